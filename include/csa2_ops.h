@@ -1,0 +1,92 @@
+/*
+ * csa2_ops.h -- C ABI of libcsa2.so, the operators around the paged cache of
+ * csa2.h: what turns a layer's projections into rotated queries and cache
+ * rows, dense attention of new tokens over the whole cache, and the eviction
+ * of entries by the attention weight that they have received.
+ *
+ * The conventions of csa2.h hold: device pointers owned by the caller, host
+ * validation before any launch, no allocation or synchronisation, work
+ * enqueued on `stream`, data-dependent violations recorded in
+ * cache->err_word and never trapping.
+ */
+#ifndef CSA2_OPS_H
+#define CSA2_OPS_H
+
+#include "csa2.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element type of an argument that may have either. */
+typedef enum { CSA2_BF16 = 0, CSA2_F32 = 1 } csa2_dtype;
+
+/*
+ * Rotation of the LAST `rot` channels of a row of dim channels by its
+ * position: pair i is turned by the angle pos * freqs[i],
+ *   (u, v) -> (u cos - v sin, u sin + v cos).
+ * The pairs are channels (dim - rot + 2i, dim - rot + 2i + 1) when
+ * interleaved != 0, else (dim - rot + i, dim - rot/2 + i).  Angles are formed
+ * in float64: in fp32 the angle of position 10^6 is off by up to 0.03.
+ *   freqs  float64 [rot / 2] device, radians per position (8-byte aligned;
+ *          NULL when rot == 0)
+ *   rot    0 .. dim, a multiple of 32
+ */
+typedef struct csa2_rope {
+  const double* freqs;
+  int32_t rot;
+  int32_t interleaved;
+} csa2_rope;
+
+/*
+ * csa2_norm_rope -- RMS norm of every head and rotation, in one pass:
+ *   y = x * weight / sqrt(mean(x^2) + eps), then the rotation above.
+ * fp32 arithmetic (angles float64), one rounding to the output's type.
+ *   n_rows    tokens (0 does nothing);  heads >= 1;  dim 128 or 512
+ *   x         [n_rows] rows of `heads` x `dim` elements of x_type (16-byte
+ *             aligned); consecutive rows are x_stride elements apart
+ *             (x_stride >= heads * dim and a multiple of 16 bytes)
+ *   weight    float [dim], the same for every head, or NULL (ones); 16-byte
+ *             aligned
+ *   eps       in [1e-12, 1]
+ *   pos       int32 [n_rows] position of each row (any value)
+ *   out       [n_rows][heads][dim] of out_type, contiguous, 16-byte aligned.
+ *             It may be x itself when the type and the layout are the same;
+ *             it must not overlap x in any other way.
+ * A row that holds a NaN or an infinity follows the formula (NaN where the
+ * value is not finite, 0 or NaN elsewhere).
+ */
+CSA2_API csa2_status csa2_norm_rope(int32_t n_rows, int32_t heads, int32_t dim, const void* x, csa2_dtype x_type,
+                                    int64_t x_stride, const float* weight, float eps, const csa2_rope* rope,
+                                    const int32_t* pos, void* out, csa2_dtype out_type, void* stream);
+
+/*
+ * csa2_norm_rope_append -- norm, rotation and quantise-on-append of new cache
+ * rows in one pass: main-KV row kv[i] (512) and indexer key ik[i] (128) are
+ * normed (each over its own row) and rotated in float64, rounded once to
+ * fp32, and stored exactly as csa2_append_kv stores fp32 rows; with ik4 the
+ * indexer key is also stored as csa2_append_ik4 stores it.
+ *   kv, ik     rows of `type` elements (16-byte aligned), kv_stride and
+ *              ik_stride elements apart (multiples of 16 bytes): they may be
+ *              slices of one projection's output
+ *   kv_weight  float [512] or NULL, ik_weight float [128] or NULL (16-byte
+ *              aligned);  eps in [1e-12, 1]
+ *   kv_rope, ik_rope  the rotation of each kind of row
+ *   rope_pos   int32 [n_rows] positions for the rotation; NULL: pos (after
+ *              an eviction a token's slot is no longer its position)
+ *   req, pos   as csa2_append_kv: the slot of each row.  No two rows of one
+ *              call may have the same slot.
+ * ctx_len is not modified.  Device errors as csa2_append_kv.
+ */
+CSA2_API csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_ik4* ik4, int32_t n_rows,
+                                           csa2_dtype type, const void* kv, int64_t kv_stride, const void* ik,
+                                           int64_t ik_stride, const float* kv_weight, const float* ik_weight,
+                                           float eps, const csa2_rope* kv_rope, const csa2_rope* ik_rope,
+                                           const int32_t* rope_pos, const int32_t* req, const int32_t* pos,
+                                           void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* CSA2_OPS_H */

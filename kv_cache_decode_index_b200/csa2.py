@@ -1,4 +1,4 @@
-"""ctypes binding of libcsa2.so (include/csa2.h).
+"""ctypes binding of libcsa2.so (include/csa2.h, include/csa2_ops.h).
 
 Argument marshalling only: every step of the decode path runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  There is
@@ -39,10 +39,17 @@ class Ik4Struct(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _CP = ctypes.POINTER(CacheStruct)
 _KP = ctypes.POINTER(Ik4Struct)
+_RP = ctypes.POINTER(RopeStruct)
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _sig = {
     "csa2_append_kv": [_CP, _I, _P, _P, _P, _P, _P],
     "csa2_compress_append": [_CP, _I, _I, _P, _P, _P, _P, _P],
@@ -61,6 +68,8 @@ _sig = {
     "csa2_sparse_attn_swa": [_CP, _I, _P, _P, _I, _P, _P, _I, _P, _P, _I, ctypes.c_float, _P, _P],
     "csa2_prefill_index": [_CP, _I, _I, _P, _I, _P, _P, _I, _P, _P, ctypes.c_size_t, _P],
     "csa2_prefill_index_static": [_CP, _I, _I, _P, _I, _P, _P, _I, _P, _P],
+    "csa2_norm_rope": [_I, _I, _I, _P, _I, _L, _P, _F, _RP, _P, _P, _I, _P],
+    "csa2_norm_rope_append": [_CP, _KP, _I, _I, _P, _L, _P, _L, _P, _P, _F, _RP, _RP, _P, _P, _P, _P],
     "csa2_get_error": [_CP, ctypes.POINTER(ctypes.c_int32), _P],
 }
 for _name, _args in _sig.items():
@@ -104,6 +113,14 @@ def _need(t, dtype, shape, name):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device.type != "cuda":
         raise ValueError(f"{name}: expected contiguous cuda {dtype} {tuple(shape)}, "
                          f"got {t.device} {t.dtype} {tuple(t.shape)}")
+
+
+def _arg(t, dtype, shape, name, dev):
+    """_need, and on device `dev` (the one the call runs on); None passes."""
+    if t is not None:
+        _need(t, dtype, shape, name)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
 
 
 def set_wait_limit_ns(ns: int):
@@ -467,6 +484,86 @@ def sparse_attn_swa(cache: Cache, topk, swa: SwaKV, q_pos, q, scale: float | Non
                                      _ptr(swa.exp), swa.window, _ptr(q_pos), _ptr(q), H, ctypes.c_float(scale),
                                      _ptr(out), _stream(cache.device)), "csa2_sparse_attn_swa")
     return out
+
+
+class Rope:
+    """Rotation of a row's last 2 * len(freqs) channels by its position:
+    freqs float64 [rot / 2] (radians per position; rot a multiple of 32, or
+    None for no rotation); interleaved: pairs of neighbouring channels, else
+    the two halves of the rotated part."""
+
+    def __init__(self, freqs=None, interleaved: bool = True):
+        if freqs is not None:
+            _need(freqs, torch.float64, (freqs.numel(),), "freqs")
+        self.freqs, self.rot, self.interleaved = freqs, 0 if freqs is None else 2 * freqs.numel(), bool(interleaved)
+        self.struct = RopeStruct(freqs.data_ptr() if self.rot else None, self.rot, int(self.interleaved))
+
+
+_DTYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _rows(t, shape, name, dev):
+    """Rows of bf16 / fp32 elements, dense inside a row; returns the distance
+    between rows in elements."""
+    inner = 1
+    ok = t.dtype in _DTYPE and tuple(t.shape) == tuple(shape) and t.device.type == "cuda" and t.device == dev
+    for d in range(t.dim() - 1, 0, -1):
+        ok = ok and (t.stride(d) == inner or t.shape[d] == 1)
+        inner *= t.shape[d]
+    if not ok:
+        raise ValueError(f"{name}: expected bf16 or fp32 rows of shape {tuple(shape)} on {dev}, dense inside a row, "
+                         f"got {t.device} {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else inner
+
+
+def norm_rope(x, pos, rope: Rope, weight=None, eps: float = 1e-6, out=None, out_dtype=None):
+    """RMS norm of every head of x [n, H, D] (D 128 or 512, bf16 or fp32; rows
+    may be slices of a wider tensor) and rotation by pos int32 [n]; returns
+    out [n, H, D] in out_dtype (default: x's type; out may be x)."""
+    n, H, D = x.shape
+    dev = x.device
+    stride = _rows(x, (n, H, D), "x", dev)
+    _arg(pos, torch.int32, (n,), "pos", dev)
+    _arg(weight, torch.float32, (D,), "weight", dev)
+    _arg(rope.freqs, torch.float64, (rope.rot // 2,), "rope.freqs", dev)
+    if out is None:
+        out = torch.empty(n, H, D, dtype=out_dtype or x.dtype, device=dev)
+    if out.dtype not in _DTYPE:
+        raise ValueError(f"out: expected bf16 or fp32, got {out.dtype}")
+    _arg(out, out_dtype or out.dtype, (n, H, D), "out", dev)
+    with torch.cuda.device(dev):
+        _check(_lib.csa2_norm_rope(n, H, D, _ptr(x), _DTYPE[x.dtype], stride, _ptr(weight), eps,
+                                   ctypes.byref(rope.struct), _ptr(pos), _ptr(out), _DTYPE[out.dtype],
+                                   _stream(dev)), "csa2_norm_rope")
+    return out
+
+
+def norm_rope_append(cache: Cache, kv, ik, pos, kv_rope: Rope, ik_rope: Rope, rope_pos=None, kv_weight=None,
+                     ik_weight=None, eps: float = 1e-6, req=None, ik4: Ik4 | None = None):
+    """Norm, rotation and quantise-on-append of new rows kv [n, 512] / ik
+    [n, 128] (bf16 or fp32, the same type; rows may be slices of a wider
+    tensor) at slots pos of requests req; rope_pos int32 [n]: positions for
+    the rotation (default pos).  With ik4 the indexer keys are also stored in
+    the FP4 indexer format."""
+    n = kv.shape[0]
+    dev = cache.err_word.device
+    kv_stride, ik_stride = _rows(kv, (n, KV_DIM), "kv", dev), _rows(ik, (n, INDEX_DIM), "ik", dev)
+    if kv.dtype != ik.dtype:
+        raise ValueError(f"kv and ik differ in type: {kv.dtype}, {ik.dtype}")
+    _arg(pos, torch.int32, (n,), "pos", dev)
+    _arg(rope_pos, torch.int32, (n,), "rope_pos", dev)
+    _arg(req, torch.int32, (n,), "req", dev)
+    _arg(kv_weight, torch.float32, (KV_DIM,), "kv_weight", dev)
+    _arg(ik_weight, torch.float32, (INDEX_DIM,), "ik_weight", dev)
+    _arg(kv_rope.freqs, torch.float64, (kv_rope.rot // 2,), "kv_rope.freqs", dev)
+    _arg(ik_rope.freqs, torch.float64, (ik_rope.rot // 2,), "ik_rope.freqs", dev)
+    with torch.cuda.device(dev):
+        _check(_lib.csa2_norm_rope_append(ctypes.byref(cache.struct),
+                                          None if ik4 is None else ctypes.byref(ik4.struct), n, _DTYPE[kv.dtype],
+                                          _ptr(kv), kv_stride, _ptr(ik), ik_stride, _ptr(kv_weight),
+                                          _ptr(ik_weight), eps, ctypes.byref(kv_rope.struct),
+                                          ctypes.byref(ik_rope.struct), _ptr(rope_pos), _ptr(req), _ptr(pos),
+                                          _stream(dev)), "csa2_norm_rope_append")
 
 
 def get_error(cache: Cache):

@@ -1,4 +1,4 @@
-// C ABI of libcsa2.so (declared in include/csa2.h): host-side validation,
+// C ABI of libcsa2.so (declared in include/csa2.h and include/csa2_ops.h): host-side validation,
 // TMA tensor maps, launches.  No allocation, no synchronisation except in
 // csa2_get_error.
 #include <cuda.h>
@@ -140,6 +140,32 @@ csa2_status check_cache(const csa2_cache* c, bool need_kv, bool need_ik) {
     const csa2_status s_ = (expr);     \
     if (s_ != CSA2_OK) return s_;      \
   } while (0)
+
+constexpr int kMaxNormHeads = 4096;
+
+csa2_status check_dtype(csa2_dtype t) {
+  return t == CSA2_BF16 || t == CSA2_F32 ? CSA2_OK : fail(CSA2_ERR_ARG, "unknown element type %d", static_cast<int>(t));
+}
+
+csa2_status check_rope(const csa2_rope* r, int dim, const char* name) {
+  if (r == nullptr) return fail(CSA2_ERR_ARG, "%s must be set", name);
+  if (r->rot < 0 || r->rot > dim || r->rot % 32 != 0)
+    return fail(CSA2_ERR_SHAPE, "%s.rot %d must be a multiple of 32 in [0, %d]", name, r->rot, dim);
+  if (r->rot > 0 && (r->freqs == nullptr || !aligned(r->freqs, 8)))
+    return fail(CSA2_ERR_ARG, "%s.freqs must be set and 8-byte aligned", name);
+  return CSA2_OK;
+}
+
+csa2_status check_eps(float eps) {   // also refuses NaN
+  if (!(eps >= 1e-12f && eps <= 1.0f)) return fail(CSA2_ERR_SHAPE, "eps %g outside [1e-12, 1]", static_cast<double>(eps));
+  return CSA2_OK;
+}
+
+csa2_status check_stride(long long stride, long long width, csa2_dtype t, const char* name) {
+  if (stride < width || stride % (t == CSA2_BF16 ? 8 : 4) != 0)
+    return fail(CSA2_ERR_SHAPE, "%s %lld must be at least %lld elements and a multiple of 16 bytes", name, stride, width);
+  return CSA2_OK;
+}
 
 csa2_status sparse_attn_impl(const csa2_cache* cache, int32_t n_layers, int32_t n_queries, const int32_t* q_req,
                              const int32_t* const* topk, int32_t k, const uint16_t* const* q, int32_t H, float scale,
@@ -540,6 +566,55 @@ csa2_status csa2_prefill_index_static(const csa2_cache* cache, int32_t req, int3
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetSymbolAddress(prefill scratch)");
   return csa2_prefill_index(cache, req, n_queries, q_pos, ratio, q, w, k, topk, scratch,
                             csa2::prefill_workspace_bytes(n_queries), stream);
+}
+
+csa2_status csa2_norm_rope(int32_t n_rows, int32_t heads, int32_t dim, const void* x, csa2_dtype x_type,
+                           int64_t x_stride, const float* weight, float eps, const csa2_rope* rope,
+                           const int32_t* pos, void* out, csa2_dtype out_type, void* stream) {
+  if (n_rows < 0) return fail(CSA2_ERR_SHAPE, "n_rows %d < 0", n_rows);
+  if (dim != csa2::kIndexDim && dim != csa2::kKvDim) return fail(CSA2_ERR_SHAPE, "dim %d not in {128, 512}", dim);
+  if (heads < 1 || heads > kMaxNormHeads) return fail(CSA2_ERR_SHAPE, "heads %d outside [1, %d]", heads, kMaxNormHeads);
+  CSA2_TRY(check_dtype(x_type));
+  CSA2_TRY(check_dtype(out_type));
+  CSA2_TRY(check_rope(rope, dim, "rope"));
+  CSA2_TRY(check_eps(eps));
+  CSA2_TRY(check_stride(x_stride, static_cast<long long>(heads) * dim, x_type, "x_stride"));
+  if (n_rows == 0) return CSA2_OK;
+  if (x == nullptr || out == nullptr || pos == nullptr || !aligned(x, 16) || !aligned(out, 16) || !aligned(weight, 16))
+    return fail(CSA2_ERR_ARG, "x, out (16-byte aligned) and pos must be set, weight 16-byte aligned");
+  DeviceInfo d;
+  CSA2_TRY(device_info(&d));
+  const cudaError_t e = csa2::launch_norm_rope(n_rows, heads, dim, x, x_type, x_stride, weight, eps, *rope, pos, out,
+                                               out_type, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "norm_rope launch");
+}
+
+csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_ik4* ik4, int32_t n_rows, csa2_dtype type,
+                                  const void* kv, int64_t kv_stride, const void* ik, int64_t ik_stride,
+                                  const float* kv_weight, const float* ik_weight, float eps,
+                                  const csa2_rope* kv_rope, const csa2_rope* ik_rope, const int32_t* rope_pos,
+                                  const int32_t* req, const int32_t* pos, void* stream) {
+  CSA2_TRY(check_cache(cache, true, true));
+  if (ik4 != nullptr) CSA2_TRY(check_ik4(ik4));
+  if (n_rows < 0) return fail(CSA2_ERR_SHAPE, "n_rows %d < 0", n_rows);
+  CSA2_TRY(check_dtype(type));
+  CSA2_TRY(check_rope(kv_rope, csa2::kKvDim, "kv_rope"));
+  CSA2_TRY(check_rope(ik_rope, csa2::kIndexDim, "ik_rope"));
+  CSA2_TRY(check_eps(eps));
+  CSA2_TRY(check_stride(kv_stride, csa2::kKvDim, type, "kv_stride"));
+  CSA2_TRY(check_stride(ik_stride, csa2::kIndexDim, type, "ik_stride"));
+  if (n_rows == 0) return CSA2_OK;
+  if (kv == nullptr || ik == nullptr || pos == nullptr || !aligned(kv, 16) || !aligned(ik, 16) ||
+      !aligned(kv_weight, 16) || !aligned(ik_weight, 16))
+    return fail(CSA2_ERR_ARG, "kv, ik (16-byte aligned) and pos must be set, the weights 16-byte aligned");
+  if (req == nullptr && n_rows > cache->batch)
+    return fail(CSA2_ERR_SHAPE, "without req, n_rows (%d) must not exceed batch (%d)", n_rows, cache->batch);
+  DeviceInfo d;
+  CSA2_TRY(device_info(&d));
+  const cudaError_t e = csa2::launch_norm_rope_append(*cache, ik4, n_rows, type, kv, kv_stride, ik, ik_stride, kv_weight,
+                                                      ik_weight, eps, *kv_rope, *ik_rope, rope_pos, req, pos,
+                                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "norm_rope_append launch");
 }
 
 csa2_status csa2_get_error(const csa2_cache* cache, int32_t* out, void* stream) {

@@ -32,7 +32,7 @@
 // Every wait is bounded (CSA2_ERR_TIMEOUT, drain, free tensor memory, return).
 #include <cub/block/block_scan.cuh>
 
-#include "fp4.cuh"
+#include "append_row.cuh"
 #include "launch.h"
 #include "scan_units.cuh"
 
@@ -462,12 +462,7 @@ __global__ void __launch_bounds__(256) append_ik4_kernel(csa2_cache cache, uint8
   }
   const long long row = static_cast<long long>(page) * cache.page_size + t % cache.page_size;
   const float4 v = reinterpret_cast<const float4*>(ik_new + static_cast<long long>(warp) * kIndexDim)[lane];
-  uint32_t sc;
-  const uint32_t c = fp4_row_lane(v, &sc);
-  reinterpret_cast<uint16_t*>(codes + row * kCodeBytes)[lane] = static_cast<uint16_t>(c);
-  if ((lane & 3) == 0)
-    scales[(row / kTile) * kTileScaleBytes + block_scale_offset(static_cast<uint32_t>(row % kTile), lane >> 2)] =
-        static_cast<uint8_t>(sc);
+  store_ik4(codes, scales, row, v, lane);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/csa2.h"
+#include "../../include/csa2_ops.h"
 
 namespace csa2 {
 
@@ -120,5 +121,15 @@ cudaError_t launch_sparse_attn(const csa2_cache& cache, int n_layers, int n_quer
 size_t attn_workspace_bytes(long long n_layers, long long n_queries, int H);
 cudaError_t launch_swa_append(const csa2_cache& cache, int window, uint8_t* swa_codes, uint8_t* swa_exp, int n_rows,
                               const float* x, const int32_t* req, const int32_t* pos, cudaStream_t stream);
+
+// Per-head norm + rotation of queries; the same fused into quantise-on-append.
+cudaError_t launch_norm_rope(int n_rows, int heads, int dim, const void* x, csa2_dtype x_type, long long x_stride,
+                             const float* weight, float eps, const csa2_rope& rope, const int32_t* pos, void* out,
+                             csa2_dtype out_type, cudaStream_t stream);
+cudaError_t launch_norm_rope_append(const csa2_cache& cache, const csa2_ik4* ik4, int n_rows, csa2_dtype type,
+                                    const void* kv, long long kv_stride, const void* ik, long long ik_stride,
+                                    const float* kv_weight, const float* ik_weight, float eps,
+                                    const csa2_rope& kv_rope, const csa2_rope& ik_rope, const int32_t* rope_pos,
+                                    const int32_t* req, const int32_t* pos, cudaStream_t stream);
 
 }  // namespace csa2

@@ -1,0 +1,70 @@
+"""Refusals of the cache operators (include/csa2_ops.h) on the host: no device
+is touched."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from tests.test_abi import _cache, lib  # noqa: F401
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+F32 = ctypes.c_float
+
+
+def test_every_operator_is_exported(lib):  # noqa: F811
+    text = open(os.path.join(ROOT, "include", "csa2_ops.h")).read()
+    names = re.findall(r"CSA2_API\s+[\w\s\*]+?\b(csa2_\w+)\s*\(", text)
+    assert names
+    so = ctypes.CDLL(lib.LIB_PATH)
+    for n in names:
+        assert hasattr(so, n), f"{n} missing from libcsa2.so"
+
+
+def test_norm_rope_refusals(lib):  # noqa: F811
+    _, p = _cache(lib)
+    P, f = ctypes.c_void_p(p), lib._lib.csa2_norm_rope
+    rope = lambda rot=64, fr=p: ctypes.byref(lib.RopeStruct(fr, rot, 1))  # noqa: E731
+
+    def call(n=1, H=2, D=128, x=P, xt=0, stride=256, w=P, eps=1e-6, r=None, pos=P, out=P, ot=0):
+        return f(n, H, D, x, xt, stride, w, F32(eps), rope() if r is None else r, pos, out, ot, None)
+    assert call(n=-1) == lib.ERR_SHAPE and call(D=256) == lib.ERR_SHAPE and call(H=0) == lib.ERR_SHAPE
+    assert call(stride=255) == lib.ERR_SHAPE and call(stride=260) == lib.ERR_SHAPE      # 260 bf16: not 16 bytes
+    assert call(xt=2) == lib.ERR_ARG and call(ot=-1) == lib.ERR_ARG
+    assert call(eps=0.0) == lib.ERR_SHAPE and call(eps=float("nan")) == lib.ERR_SHAPE
+    assert call(r=rope(48)) == lib.ERR_SHAPE and call(r=rope(160)) == lib.ERR_SHAPE
+    assert call(r=rope(64, None)) == lib.ERR_ARG and call(r=rope(64, p + 4)) == lib.ERR_ARG
+    assert call(x=None) == lib.ERR_ARG and call(out=ctypes.c_void_p(p + 8)) == lib.ERR_ARG
+    assert call(pos=None) == lib.ERR_ARG and call(w=ctypes.c_void_p(p + 4)) == lib.ERR_ARG
+    assert call(n=0, x=None, out=None, pos=None) == lib.OK
+
+
+def test_norm_rope_append_refusals(lib):  # noqa: F811
+    c, p = _cache(lib)
+    P, f = ctypes.c_void_p(p), lib._lib.csa2_norm_rope_append
+    good = lib.RopeStruct(p, 64, 1)
+
+    def call(cache=c, ik4=None, n=2, t=1, kv=P, ks=640, ik=P, is_=640, eps=1e-6, kr=good, ir=good, req=P, pos=P):
+        return f(ctypes.byref(cache), ik4, n, t, kv, ks, ik, is_, None, None, F32(eps), ctypes.byref(kr),
+                 ctypes.byref(ir), None, req, pos, None)
+    bad, _ = _cache(lib, page_size=100)
+    assert call(cache=bad) == lib.ERR_SHAPE
+    assert call(ik4=ctypes.byref(lib.Ik4Struct(None, None))) == lib.ERR_ARG
+    assert call(n=-1) == lib.ERR_SHAPE and call(t=5) == lib.ERR_ARG
+    assert call(ks=511) == lib.ERR_SHAPE and call(is_=130) == lib.ERR_SHAPE
+    assert call(ir=lib.RopeStruct(p, 256, 1)) == lib.ERR_SHAPE and call(eps=2.0) == lib.ERR_SHAPE
+    assert call(kv=None) == lib.ERR_ARG and call(ik=ctypes.c_void_p(p + 4)) == lib.ERR_ARG
+    assert call(pos=None) == lib.ERR_ARG
+    assert call(n=3, req=None) == lib.ERR_SHAPE
+    assert call(n=0, kv=None, ik=None, pos=None) == lib.OK
+
+
+def test_binding_refuses_tensors(lib):  # noqa: F811
+    x, pos = torch.zeros(2, 4, 128), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        lib.norm_rope(x, pos, lib.Rope())                      # not on a GPU
+    with pytest.raises(ValueError):
+        lib.Rope(torch.zeros(32, dtype=torch.float32))
+    with pytest.raises(ValueError):
+        lib._rows(torch.zeros(2, 4, 128).transpose(1, 2), (2, 128, 4), "x", torch.device("cpu"))

@@ -85,6 +85,44 @@ CSA2_API csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_i
                                            const int32_t* rope_pos, const int32_t* req, const int32_t* pos,
                                            void* stream);
 
+/*
+ * csa2_chunk_attn -- dense attention of new tokens over the paged cache
+ * (K = V = the dequantised main-KV row, one for all heads):
+ *   out = sum_e softmax_e(scale q . v_e) v_e,  lse = ln sum_e exp(scale q . v_e)
+ * over the entries e that the query sees: e < min(ctx_len[b],
+ * floor((q_pos + 1) / ratio)), the causal rule of csa2_prefill_index.  The new
+ * tokens' own rows are appended first; ctx_len counts them.  A query that sees
+ * nothing has out = 0 and lse = -inf.
+ *   q_start  int32 [batch + 1]: request b's queries are rows q_start[b] ..
+ *            q_start[b + 1] - 1 (ascending; 0 .. any number of them).  Rows
+ *            from q_start[batch] on (a padded batch) are left untouched.  NULL:
+ *            query i belongs to request i (n_queries <= batch), one new token
+ *            each.
+ *   q_pos    int32 [n_queries] token position of each query (negative: sees
+ *            nothing; any order)
+ *   ratio    tokens per entry, >= 1
+ *   q, out   bf16 [n_queries][H][512], 16-byte aligned; H in {16, 32, 64}.
+ *            out must not overlap q
+ *   lse      float [n_queries][H] or NULL
+ *   n_queries <= 2^20
+ *   workspace  at least csa2_chunk_attn_workspace_bytes bytes, 16-byte
+ *            aligned; its contents on entry do not matter.  Two calls in
+ *            flight at once must not share it.
+ * Dequantised rows are exact in fp16; scores, softmax and sums are fp32, the
+ * probabilities are rounded to fp16 for the product with V.  Long contexts are
+ * cut along the keys by a plan made of the lengths alone: the same lengths
+ * give the same bits.
+ * Device errors: a page id outside [0, num_pages) under a visible entry
+ * (CSA2_ERR_DEVICE_BOUNDS; its entries are left out), a q_start that
+ * decreases or leaves [0, n_queries] (the request has no queries), a ctx_len
+ * outside [0, capacity] (its queries see nothing).
+ */
+CSA2_API size_t csa2_chunk_attn_workspace_bytes(int32_t batch, int32_t n_queries, int32_t H);
+CSA2_API csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries, const int32_t* q_start,
+                                     const int32_t* q_pos, int32_t ratio, const uint16_t* q, int32_t H, float scale,
+                                     uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif

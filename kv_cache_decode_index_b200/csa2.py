@@ -70,6 +70,7 @@ _sig = {
     "csa2_prefill_index_static": [_CP, _I, _I, _P, _I, _P, _P, _I, _P, _P],
     "csa2_norm_rope": [_I, _I, _I, _P, _I, _L, _P, _F, _RP, _P, _P, _I, _P],
     "csa2_norm_rope_append": [_CP, _KP, _I, _I, _P, _L, _P, _L, _P, _P, _F, _RP, _RP, _P, _P, _P, _P],
+    "csa2_chunk_attn": [_CP, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, ctypes.c_size_t, _P],
     "csa2_get_error": [_CP, ctypes.POINTER(ctypes.c_int32), _P],
 }
 for _name, _args in _sig.items():
@@ -85,6 +86,8 @@ _lib.csa2_attn_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.csa2_attn_workspace_bytes.restype = ctypes.c_size_t
 _lib.csa2_reindex_layers_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.csa2_reindex_layers_workspace_bytes.restype = ctypes.c_size_t
+_lib.csa2_chunk_attn_workspace_bytes.argtypes = [_I, _I, _I]
+_lib.csa2_chunk_attn_workspace_bytes.restype = ctypes.c_size_t
 _lib.csa2_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.csa2_set_wait_limit_ns.restype = None
 
@@ -564,6 +567,42 @@ def norm_rope_append(cache: Cache, kv, ik, pos, kv_rope: Rope, ik_rope: Rope, ro
                                           _ptr(ik_weight), eps, ctypes.byref(kv_rope.struct),
                                           ctypes.byref(ik_rope.struct), _ptr(rope_pos), _ptr(req), _ptr(pos),
                                           _stream(dev)), "csa2_norm_rope_append")
+
+
+def _workspace(ws, need, dev):
+    if ws is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != dev:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {dev}")
+    return ws
+
+
+def chunk_attn_workspace_bytes(cache: Cache, n_queries: int, heads: int) -> int:
+    return int(_lib.csa2_chunk_attn_workspace_bytes(cache.batch, int(n_queries), int(heads)))
+
+
+def chunk_attn(cache: Cache, q, q_pos, q_start=None, ratio: int = 1, scale: float | None = None, out=None, lse=None,
+               workspace=None):
+    """Dense attention of new tokens over the paged cache: q bf16 [n, H, 512],
+    q_pos int32 [n] token positions; q_start int32 [batch + 1]: request b's
+    queries are rows q_start[b] .. q_start[b + 1] - 1 (None: query i is
+    request i's).  lse: optional float32 [n, H] to fill.  Returns out."""
+    n, H = q.shape[0], q.shape[1]
+    dev = cache.err_word.device
+    _arg(q, torch.bfloat16, (n, H, KV_DIM), "q", dev)
+    _arg(q_pos, torch.int32, (n,), "q_pos", dev)
+    _arg(q_start, torch.int32, (cache.batch + 1,), "q_start", dev)
+    if out is None:
+        out = torch.empty_like(q)
+    _arg(out, torch.bfloat16, (n, H, KV_DIM), "out", dev)
+    _arg(lse, torch.float32, (n, H), "lse", dev)
+    scale = 1.0 / math.sqrt(KV_DIM) if scale is None else scale
+    with torch.cuda.device(dev):
+        workspace = _workspace(workspace, chunk_attn_workspace_bytes(cache, n, H), dev)
+        _check(_lib.csa2_chunk_attn(ctypes.byref(cache.struct), n, _ptr(q_start), _ptr(q_pos), int(ratio), _ptr(q), H,
+                                    scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(dev)),
+               "csa2_chunk_attn")
+    return out
 
 
 def get_error(cache: Cache):

@@ -24,7 +24,8 @@ constexpr int kPoolHistBits = 12;
 static_assert(kPoolHistBins == 1 << kPoolHistBits, "one bin per leading-bit pattern");
 
 // kernel ids recorded in err_word[1]
-enum KernelId { kKAppend = 1, kKIndexFull = 2, kKPoolSelect = 3, kKReindex = 4, kKAttn = 5, kKPrefill = 6 };
+enum KernelId { kKAppend = 1, kKIndexFull = 2, kKPoolSelect = 3, kKReindex = 4, kKAttn = 5, kKPrefill = 6, kKChunk = 7, kKMass = 8,
+                kKEvict = 9 };
 
 // Wait bound of the pipeline barriers (ns of %globaltimer).  Well above any
 // legitimate wait; a wait that runs out records CSA2_ERR_TIMEOUT and the CTA

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -142,6 +143,7 @@ csa2_status check_cache(const csa2_cache* c, bool need_kv, bool need_ik) {
   } while (0)
 
 constexpr int kMaxNormHeads = 4096;
+constexpr int kMaxDenseQueries = 1 << 20;
 
 csa2_status check_dtype(csa2_dtype t) {
   return t == CSA2_BF16 || t == CSA2_F32 ? CSA2_OK : fail(CSA2_ERR_ARG, "unknown element type %d", static_cast<int>(t));
@@ -164,6 +166,25 @@ csa2_status check_eps(float eps) {   // also refuses NaN
 csa2_status check_stride(long long stride, long long width, csa2_dtype t, const char* name) {
   if (stride < width || stride % (t == CSA2_BF16 ? 8 : 4) != 0)
     return fail(CSA2_ERR_SHAPE, "%s %lld must be at least %lld elements and a multiple of 16 bytes", name, stride, width);
+  return CSA2_OK;
+}
+
+// What the dense operators (chunk_attn, attn_mass) share.
+csa2_status check_dense(const csa2_cache* c, int n_queries, const int32_t* q_start, int ratio, int H, float scale) {
+  CSA2_TRY(check_cache(c, true, false));
+  if (n_queries < 0 || n_queries > kMaxDenseQueries)
+    return fail(CSA2_ERR_SHAPE, "n_queries %d outside [0, %d]", n_queries, kMaxDenseQueries);
+  if (q_start == nullptr && n_queries > c->batch)
+    return fail(CSA2_ERR_SHAPE, "without q_start, n_queries (%d) must not exceed batch (%d)", n_queries, c->batch);
+  if (ratio < 1) return fail(CSA2_ERR_SHAPE, "ratio %d < 1", ratio);
+  if (H != 16 && H != 32 && H != 64) return fail(CSA2_ERR_SHAPE, "H %d not in {16, 32, 64}", H);
+  if (!std::isfinite(scale)) return fail(CSA2_ERR_ARG, "scale must be finite");
+  return CSA2_OK;
+}
+
+csa2_status check_workspace(const void* ws, size_t bytes, size_t need, const char* fn) {
+  if (ws == nullptr || !aligned(ws, 16)) return fail(CSA2_ERR_ARG, "workspace must be set and 16-byte aligned");
+  if (bytes < need) return fail(CSA2_ERR_SHAPE, "workspace_bytes %zu < %zu (%s)", bytes, need, fn);
   return CSA2_OK;
 }
 
@@ -615,6 +636,27 @@ csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_ik4* ik4, 
                                                       ik_weight, eps, *kv_rope, *ik_rope, rope_pos, req, pos,
                                                       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "norm_rope_append launch");
+}
+
+size_t csa2_chunk_attn_workspace_bytes(int32_t batch, int32_t n_queries, int32_t H) {
+  if (batch < 1 || n_queries < 1 || H < 1) return 0;
+  return csa2::chunk_attn_workspace_bytes();
+}
+
+csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries, const int32_t* q_start, const int32_t* q_pos,
+                            int32_t ratio, const uint16_t* q, int32_t H, float scale, uint16_t* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  CSA2_TRY(check_dense(cache, n_queries, q_start, ratio, H, scale));
+  if (n_queries == 0) return CSA2_OK;
+  if (q_pos == nullptr || q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16))
+    return fail(CSA2_ERR_ARG, "q_pos, q and out (16-byte aligned) must be set");
+  CSA2_TRY(check_workspace(workspace, workspace_bytes, csa2_chunk_attn_workspace_bytes(cache->batch, n_queries, H),
+                           "csa2_chunk_attn_workspace_bytes"));
+  DeviceInfo d;
+  CSA2_TRY(device_info(&d));
+  const cudaError_t e = csa2::launch_chunk_attn(*cache, n_queries, q_start, q_pos, ratio, q, H, scale, out, lse, workspace,
+                                                d.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "chunk_attn launch");
 }
 
 csa2_status csa2_get_error(const csa2_cache* cache, int32_t* out, void* stream) {

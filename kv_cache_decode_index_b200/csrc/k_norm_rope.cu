@@ -214,11 +214,6 @@ __global__ void __launch_bounds__(kNThreads)
 // up to the rounding to fp32 is float64, so that the stored codes are those of
 // the formula itself: an fp32 norm, off by 1e-7, would move values across the
 // FP4 and FP8 borders.
-template <typename T>
-__device__ __forceinline__ double value_of(T v);
-template <>
-__device__ __forceinline__ double value_of(float v) { return static_cast<double>(v); }
-
 __device__ __forceinline__ double warp_sum(double s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);

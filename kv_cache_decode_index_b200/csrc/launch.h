@@ -132,4 +132,10 @@ cudaError_t launch_norm_rope_append(const csa2_cache& cache, const csa2_ik4* ik4
                                     const csa2_rope& kv_rope, const csa2_rope& ik_rope, const int32_t* rope_pos,
                                     const int32_t* req, const int32_t* pos, cudaStream_t stream);
 
+// Dense attention of new tokens over the paged cache; lse may be null.
+size_t chunk_attn_workspace_bytes();
+cudaError_t launch_chunk_attn(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
+                              int ratio, const uint16_t* q, int H, float scale, uint16_t* out, float* lse, void* ws,
+                              int num_sms, cudaStream_t stream);
+
 }  // namespace csa2

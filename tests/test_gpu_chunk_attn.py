@@ -1,0 +1,221 @@
+"""Dense attention of new tokens over the paged cache (csa2_chunk_attn)
+against its formula in float64.  Needs a B200 and libcsa2.so."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import ops_util as O
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def csa2():
+    from kv_cache_decode_index_b200 import csa2 as lib
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return lib
+
+
+def _case(csa2, lens, new, H, page, ratio=1, seed=0, pad=0, q_scale=1.0, pos=None):
+    cache, table, codes, scales = O.random_cache(csa2, lens, page, seed)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    n = int(start[-1]) + pad
+    rng = np.random.default_rng(seed + 1)
+    if pos is None:
+        pos = np.concatenate([np.arange(c * ratio - x, c * ratio) for c, x in zip(lens, new)] + [np.zeros(pad)])
+    pos = np.asarray(pos, np.int64).clip(-1).astype(np.int32)
+    # E4M3 codes 40 .. 71 are scales of 2^-2 .. 3.75: rows of norm about 100
+    q = torch.from_numpy((rng.standard_normal((n, H, 512)) * q_scale * 0.2).astype(np.float32)).bfloat16().cuda()
+    return cache, table, codes, scales, start, pos, q
+
+
+def _check(cache, table, codes, scales, start, pos, q, out, lse, lens, ratio, scale):
+    q64 = q.double().cpu().numpy()
+    got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, n_ctx in enumerate(lens):
+        a, z = int(start[b]), int(start[b + 1])
+        if a == z:
+            continue
+        seen = np.clip((pos[a:z].astype(np.int64) + 1) // ratio, 0, n_ctx)
+        K = O.keys(table, cache.page_size, codes, scales, b, n_ctx)
+        ref = O.attention(q64[a:z], K, seen, scale)
+        tol, tol_lse = O.attention_bounds(ref, max(n_ctx, 1))
+        tol = tol + torch.finfo(torch.bfloat16).eps / 2 * (np.abs(ref["out"]) + tol)
+        err = np.abs(got[a:z] - ref["out"])
+        assert (err <= tol).all(), f"request {b}: out off by {err.max():.3e}, {(err / np.maximum(tol, 1e-30)).max():.2f} of its bound"
+        none = ~np.isfinite(ref["lse"])
+        assert (got_lse[a:z][none] == -np.inf).all()
+        err = np.abs(got_lse[a:z][~none] - ref["lse"][~none])
+        assert (err <= tol_lse[~none]).all(), f"request {b}: lse off by {err.max():.3e}"
+
+
+CASES = [
+    # lens, new, page, ratio
+    ([1], [1], 128, 1),
+    ([64], [64], 128, 1),
+    ([65, 63], [65, 2], 128, 1),
+    ([129, 1, 500], [3, 1, 130], 128, 1),
+    ([300, 7, 257, 128], [5, 0, 1, 128], 256, 1),
+    ([40, 333], [80, 9], 128, 2),          # the first tokens of request 0 see no entry
+    ([200], [0], 128, 1),
+    ([1, 700], [1, 1], 384, 3),
+    ([1000, 33, 2, 515], [70, 33, 2, 1], 128, 1),
+]
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("lens,new,page,ratio", CASES)
+def test_chunk_attn(csa2, lens, new, page, ratio, H):
+    args = _case(csa2, lens, new, H, page, ratio, seed=sum(lens) + H, pad=2)
+    cache, _, _, _, start, pos, q = args
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    scale = 1 / math.sqrt(512)
+    csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda(), ratio=ratio, out=out, lse=lse)
+    st, word = csa2.get_error(cache)
+    assert st == csa2.OK, word
+    assert (out[-2:] == 7.0).all() and (lse[-2:] == 7.0).all()      # rows behind the last request
+    _check(*args, out, lse, lens, ratio, scale)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("lens", [[5000], [4097, 129, 2000], [1] * 5 + [900] * 8])
+def test_chunk_attn_single_tokens(csa2, lens, H):
+    """q_start None: one new token per request; long keys are cut and joined.
+    Twice the same bits."""
+    args = _case(csa2, lens, [1] * len(lens), H, 128, seed=len(lens))
+    cache, _, _, _, start, pos, q = args
+    lse = torch.empty(q.shape[:2], device="cuda")
+    p = torch.from_numpy(pos).cuda()
+    out = csa2.chunk_attn(cache, q, p, lse=lse)
+    _check(*args, out, lse, lens, 1, 1 / math.sqrt(512))
+    assert torch.equal(out, csa2.chunk_attn(cache, q, p))
+
+
+@pytest.mark.parametrize("H,new", [(16, 300), (32, 129), (64, 70)])
+def test_chunk_attn_positions_in_any_order(csa2, H, new):
+    """Shuffled positions, some of which see nothing, and a negative scale."""
+    rng = np.random.default_rng(4)
+    lens = [777]
+    pos = rng.integers(-3, 900, new)
+    args = _case(csa2, lens, [new], H, 128, seed=9, pos=pos)
+    cache, _, _, _, start, p, q = args
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = csa2.chunk_attn(cache, q, torch.from_numpy(p).cuda(), torch.from_numpy(start).cuda(), scale=-0.03, lse=lse)
+    _check(*args, out, lse, lens, 1, -0.03)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_chunk_attn_peaked(csa2, H):
+    """Scores far apart: one key takes nearly all the weight, and the running
+    maximum rises by much from step to step."""
+    lens, new = [640], [40]
+    args = _case(csa2, lens, new, H, 128, seed=21, q_scale=6.0)
+    cache, _, _, _, start, pos, q = args
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda(), lse=lse)
+    _check(*args, out, lse, lens, 1, 1 / math.sqrt(512))
+
+
+def test_chunk_attn_query_sizes(csa2):
+    """Rows of very large and very small queries, zeros, and one with a NaN
+    and one with an infinity: those rows are NaN, the others are not touched
+    by them."""
+    lens, new, H = [200], [6], 16
+    args = _case(csa2, lens, new, H, 128, seed=2)
+    cache, table, codes, scales, start, pos, q = args
+    q[0] *= 2.0 ** -90
+    q[1] = 0
+    q[2, 3, 5] = float("nan")
+    q[3, 1, 9] = float("inf")
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda(), lse=lse)
+    assert torch.isnan(out[2, 3]).all() and torch.isnan(out[3, 1]).all()
+    bad = torch.zeros(6, H, dtype=torch.bool, device="cuda")
+    bad[2, 3] = bad[3, 1] = True
+    assert not torch.isnan(out[~bad]).any()
+    q[2, 3], q[3, 1] = 0, 0
+    again = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda())
+    assert torch.equal(out[~bad], again[~bad])
+    lse[2, 3], lse[3, 1] = 0, 0
+    lse2 = torch.empty_like(lse)
+    csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda(), lse=lse2)
+    _check(*args, again, lse2, lens, 1, 1 / math.sqrt(512))
+    big = q.clone()
+    big[4] *= 2.0 ** 100
+    out = csa2.chunk_attn(cache, big, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda())
+    assert torch.equal(out[5], again[5]) and torch.isfinite(out[4].float()).all()
+
+
+def test_chunk_attn_recorded_violations(csa2):
+    """Bad pages, lengths and query ranges are recorded; the other requests'
+    rows are right and nothing outside is written."""
+    lens, new, H = [300, 200], [70, 3], 32
+    for what in ("page", "ctx", "start"):
+        args = _case(csa2, lens, new, H, 128, seed=5)
+        cache, table, codes, scales, start, pos, q = args
+        s = start.copy()
+        if what == "page":
+            cache.page_table[0, 1] = cache.num_pages
+        elif what == "ctx":
+            cache.ctx_len[0] = 10 ** 6
+        else:
+            s[0] = -4
+        out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(s).cuda(), out=out, lse=lse)
+        st, word = csa2.get_error(cache)
+        assert st == csa2.ERR_DEVICE_BOUNDS and word[2] == 0, (what, word)
+        if what == "ctx":
+            assert (out[:70] == 0).all() and (lse[:70] == -np.inf).all()
+        if what == "start":
+            assert (out[:70] == 7.0).all()
+        _check(cache, table, codes, scales, [70, 70, 73], pos, q, out, lse, lens, 1,
+               1 / math.sqrt(512))
+
+
+def test_chunk_attn_graph_and_stream(csa2):
+    """Captured once and replayed on changed inputs; on a side stream."""
+    lens, new, H = [700, 90], [33, 20], 32
+    args = _case(csa2, lens, new, H, 128, seed=15)
+    cache, table, codes, scales, start, pos, q = args
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    ws = torch.empty(csa2.chunk_attn_workspace_bytes(cache, q.shape[0], H), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        csa2.chunk_attn(cache, q, p, s, out=out, lse=lse, workspace=ws)
+    ws.fill_(0xFF)
+    q.copy_(q.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    _check(*args, out, lse, lens, 1, 1 / math.sqrt(512))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = csa2.chunk_attn(cache, q, p, s)
+    side.synchronize()
+    assert torch.equal(other, out)
+
+
+def test_chunk_attn_offsets_past_32_bits(csa2):
+    """Pages whose code bytes lie past 2^31 and 2^32."""
+    page, H = 4096, 16
+    num = (2 ** 32 // 256) // page + 8
+    cache = csa2.Cache(num, page, [[num - 1, num // 2 + 3]], [5000])
+    rows = O.rows_of(np.array([[num - 1, num // 2 + 3]]), page, 0, 5000)
+    rng = np.random.default_rng(0)
+    codes = rng.integers(0, 256, (5000, 256), dtype=np.uint8)
+    scales = rng.integers(40, 72, (5000, 32), dtype=np.uint8)
+    r = torch.from_numpy(rows).cuda()
+    cache.kv_codes[r] = torch.from_numpy(codes).cuda()
+    cache.kv_scales[r] = torch.from_numpy(scales).cuda()
+    q = (torch.from_numpy(rng.standard_normal((1, H, 512)).astype(np.float32)) * 0.2).bfloat16().cuda()
+    pos = np.array([4999], np.int32)
+    lse = torch.empty(1, H, device="cuda")
+    out = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), lse=lse)
+    small = np.array([[0, 1]], np.int32)      # the same rows in a small table for the reference
+    c2, s2 = np.zeros((2 * page, 256), np.uint8), np.zeros((2 * page, 32), np.uint8)
+    c2[:5000], s2[:5000] = codes, scales
+    _check(cache, small, c2, s2, [0, 1], pos, q, out, lse, [5000], 1, 1 / math.sqrt(512))

@@ -68,3 +68,24 @@ def test_binding_refuses_tensors(lib):  # noqa: F811
         lib.Rope(torch.zeros(32, dtype=torch.float32))
     with pytest.raises(ValueError):
         lib._rows(torch.zeros(2, 4, 128).transpose(1, 2), (2, 128, 4), "x", torch.device("cpu"))
+
+
+def test_chunk_attn_refusals(lib):  # noqa: F811
+    c, p = _cache(lib)
+    P, f = ctypes.c_void_p(p), lib._lib.csa2_chunk_attn
+    need = lib._lib.csa2_chunk_attn_workspace_bytes(2, 2, 64)
+    assert need > 0 and lib._lib.csa2_chunk_attn_workspace_bytes(2, 0, 64) == 0
+
+    def call(cache=c, n=2, start=P, pos=P, ratio=1, q=P, H=64, scale=0.1, out=P, ws=P, size=need):
+        return f(ctypes.byref(cache), n, start, pos, ratio, q, H, F32(scale), out, None, ws, size, None)
+    bad, _ = _cache(lib, kv_codes=p + 4)
+    assert call(cache=bad) == lib.ERR_ARG
+    assert call(n=-1) == lib.ERR_SHAPE and call(n=2 ** 20 + 1) == lib.ERR_SHAPE
+    assert call(n=3, start=None) == lib.ERR_SHAPE
+    assert call(ratio=0) == lib.ERR_SHAPE and call(H=48) == lib.ERR_SHAPE
+    assert call(scale=float("inf")) == lib.ERR_ARG and call(scale=float("nan")) == lib.ERR_ARG
+    assert call(pos=None) == lib.ERR_ARG and call(q=ctypes.c_void_p(p + 8)) == lib.ERR_ARG and call(out=None) == lib.ERR_ARG
+    assert call(ws=None) == lib.ERR_ARG and call(ws=ctypes.c_void_p(p + 8)) == lib.ERR_ARG
+    assert call(size=need - 1) == lib.ERR_SHAPE
+    assert b"csa2_chunk_attn_workspace_bytes" in lib._lib.csa2_last_error_message()
+    assert call(n=0, pos=None, q=None, out=None, ws=None, size=0) == lib.OK

@@ -123,6 +123,26 @@ CSA2_API csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries,
                                      uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/*
+ * csa2_attn_mass -- the attention weight that every cached entry received:
+ *   mass[b][e] += sum over request b's queries i and heads h of
+ *                 exp(scale q_ih . v_e - lse_ih)
+ * over the entries each query sees (the rule of csa2_chunk_attn); an entry's
+ * weights of one call sum to at most (queries) x H.  With ratio, q_start,
+ * q_pos, q, H and scale as csa2_chunk_attn took them and the lse it wrote.
+ *   mass     float [batch][capacity], added to (zero it once); entries that no
+ *            query of the call sees are untouched
+ *   workspace  at least csa2_attn_mass_workspace_bytes bytes, as above
+ * fp32 sums in an order fixed by the lengths.  Device errors as
+ * csa2_chunk_attn; a pipeline wait that runs out -> CSA2_ERR_TIMEOUT (mass is
+ * then undefined).
+ */
+CSA2_API size_t csa2_attn_mass_workspace_bytes(int32_t batch, int32_t n_queries, int32_t H);
+CSA2_API csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, const int32_t* q_start,
+                                    const int32_t* q_pos, int32_t ratio, const uint16_t* q, int32_t H, float scale,
+                                    const float* lse, float* mass, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

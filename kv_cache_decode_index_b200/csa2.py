@@ -71,6 +71,7 @@ _sig = {
     "csa2_norm_rope": [_I, _I, _I, _P, _I, _L, _P, _F, _RP, _P, _P, _I, _P],
     "csa2_norm_rope_append": [_CP, _KP, _I, _I, _P, _L, _P, _L, _P, _P, _F, _RP, _RP, _P, _P, _P, _P],
     "csa2_chunk_attn": [_CP, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, ctypes.c_size_t, _P],
+    "csa2_attn_mass": [_CP, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, ctypes.c_size_t, _P],
     "csa2_get_error": [_CP, ctypes.POINTER(ctypes.c_int32), _P],
 }
 for _name, _args in _sig.items():
@@ -88,6 +89,8 @@ _lib.csa2_reindex_layers_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.csa2_reindex_layers_workspace_bytes.restype = ctypes.c_size_t
 _lib.csa2_chunk_attn_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.csa2_chunk_attn_workspace_bytes.restype = ctypes.c_size_t
+_lib.csa2_attn_mass_workspace_bytes.argtypes = [_I, _I, _I]
+_lib.csa2_attn_mass_workspace_bytes.restype = ctypes.c_size_t
 _lib.csa2_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.csa2_set_wait_limit_ns.restype = None
 
@@ -603,6 +606,31 @@ def chunk_attn(cache: Cache, q, q_pos, q_start=None, ratio: int = 1, scale: floa
                                     scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(dev)),
                "csa2_chunk_attn")
     return out
+
+
+def attn_mass_workspace_bytes(cache: Cache, n_queries: int, heads: int) -> int:
+    return int(_lib.csa2_attn_mass_workspace_bytes(cache.batch, int(n_queries), int(heads)))
+
+
+def attn_mass(cache: Cache, q, q_pos, lse, mass, q_start=None, ratio: int = 1, scale: float | None = None,
+              workspace=None):
+    """Adds to mass float32 [batch, capacity] the attention weight that every
+    entry received from the queries (arguments as chunk_attn, with the lse it
+    wrote); returns mass."""
+    n, H = q.shape[0], q.shape[1]
+    dev = cache.err_word.device
+    _arg(q, torch.bfloat16, (n, H, KV_DIM), "q", dev)
+    _arg(q_pos, torch.int32, (n,), "q_pos", dev)
+    _arg(q_start, torch.int32, (cache.batch + 1,), "q_start", dev)
+    _arg(lse, torch.float32, (n, H), "lse", dev)
+    _arg(mass, torch.float32, (cache.batch, cache.capacity), "mass", dev)
+    scale = 1.0 / math.sqrt(KV_DIM) if scale is None else scale
+    with torch.cuda.device(dev):
+        workspace = _workspace(workspace, attn_mass_workspace_bytes(cache, n, H), dev)
+        _check(_lib.csa2_attn_mass(ctypes.byref(cache.struct), n, _ptr(q_start), _ptr(q_pos), int(ratio), _ptr(q), H,
+                                   scale, _ptr(lse), _ptr(mass), _ptr(workspace), workspace.numel(), _stream(dev)),
+               "csa2_attn_mass")
+    return mass
 
 
 def get_error(cache: Cache):

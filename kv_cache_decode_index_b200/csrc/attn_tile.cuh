@@ -50,6 +50,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 2^x (results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // cp.async (LSU path, no tensor map): 16 bytes global -> shared, completion
 // tracked per thread by commit groups.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

@@ -71,8 +71,8 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-csa2_status encode_rows_map(void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
-                            CUtensorMap* map);
+csa2_status encode_rows_map(const void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
+                            CUtensorMap* map, int box_bytes = 0);
 
 csa2_status encode_ik_map(const csa2_cache* c, int box_rows, CUtensorMap* map) {
   return encode_rows_map(c->ik_codes, static_cast<long long>(c->num_pages) * c->page_size, csa2::kIndexDim, box_rows,
@@ -80,9 +80,9 @@ csa2_status encode_ik_map(const csa2_cache* c, int box_rows, CUtensorMap* map) {
 }
 
 // 2-D map over `rows` rows of `row_bytes` bytes (uint8), box of box_rows
-// full rows.
-csa2_status encode_rows_map(void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
-                            CUtensorMap* map) {
+// rows of box_bytes bytes (0: full rows).
+csa2_status encode_rows_map(const void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
+                            CUtensorMap* map, int box_bytes) {
   static EncodeFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -95,9 +95,9 @@ csa2_status encode_rows_map(void* base, long long rows, int row_bytes, int box_r
   if (fn == nullptr) return fail(CSA2_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available");
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes ? box_bytes : row_bytes), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr,
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(CSA2_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -657,6 +657,30 @@ csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries, const in
   const cudaError_t e = csa2::launch_chunk_attn(*cache, n_queries, q_start, q_pos, ratio, q, H, scale, out, lse, workspace,
                                                 d.sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "chunk_attn launch");
+}
+
+size_t csa2_attn_mass_workspace_bytes(int32_t batch, int32_t n_queries, int32_t H) {
+  if (batch < 1 || n_queries < 1 || H < 1) return 0;
+  return csa2::attn_mass_workspace_bytes();
+}
+
+csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, const int32_t* q_start, const int32_t* q_pos,
+                           int32_t ratio, const uint16_t* q, int32_t H, float scale, const float* lse, float* mass,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  CSA2_TRY(check_dense(cache, n_queries, q_start, ratio, H, scale));
+  if (n_queries == 0) return CSA2_OK;
+  if (q_pos == nullptr || q == nullptr || lse == nullptr || mass == nullptr || !aligned(q, 16))
+    return fail(CSA2_ERR_ARG, "q_pos, q (16-byte aligned), lse and mass must be set");
+  CSA2_TRY(check_workspace(workspace, workspace_bytes, csa2_attn_mass_workspace_bytes(cache->batch, n_queries, H),
+                           "csa2_attn_mass_workspace_bytes"));
+  DeviceInfo d;
+  CSA2_TRY(device_info(&d));
+  CUtensorMap map;
+  CSA2_TRY(encode_rows_map(q, static_cast<long long>(n_queries) * H, csa2::kKvDim * 2, 32, CU_TENSOR_MAP_SWIZZLE_128B, &map,
+                           128));
+  const cudaError_t e = csa2::launch_attn_mass(*cache, n_queries, q_start, q_pos, ratio, H, scale, lse, mass, workspace,
+                                               map, d.sms, g_wait_limit_ns, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "attn_mass launch");
 }
 
 csa2_status csa2_get_error(const csa2_cache* cache, int32_t* out, void* stream) {

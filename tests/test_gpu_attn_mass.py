@@ -1,0 +1,173 @@
+"""Attention weight received by the cached entries (csa2_attn_mass) against its
+formula in float64.  Needs a B200 and libcsa2.so."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import ops_util as O
+from tests.test_gpu_chunk_attn import CASES, _case, csa2  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _reference(case, lens, ratio, scale):
+    """(lse float32 [n, H], weights [batch] of [n_ctx], bounds): a weight's
+    terms are each off by e^d - 1 <= 2 d with the scores' d (512 products
+    summed in fp32, as in attention_bounds), 2^-21 for exp2 and the product
+    with log2 e, and 2^-23 |lse| for the fp32 lse scaled to log2; summing n
+    rows adds n 2^-24 of the sum."""
+    cache, table, codes, scales, start, pos, q = case
+    q64 = q.double().cpu().numpy()
+    lse = np.zeros(q.shape[:2], np.float32)
+    mass, tol = [], []
+    for b, n_ctx in enumerate(lens):
+        a, z = int(start[b]), int(start[b + 1])
+        seen = np.clip((pos[a:z].astype(np.int64) + 1) // ratio, 0, n_ctx)
+        ref = O.attention(q64[a:z], O.keys(table, cache.page_size, codes, scales, b, n_ctx), seen, scale)
+        lse[a:z] = ref["lse"]
+        l32 = lse[a:z].astype(np.float64)
+        fine = np.isfinite(ref["s"])
+        with np.errstate(invalid="ignore"):
+            p = np.where(fine, np.exp(np.where(fine, ref["s"] - l32[..., None], 0.0)), 0.0)
+        d = (512 + 4) * 2.0 ** -23 * ref["size"] + 2.0 ** -22 + 2.0 ** -23 * np.abs(np.where(np.isfinite(l32), l32, 0.0))
+        mass.append(p.sum((0, 1)))
+        tol.append((p * 2 * d[..., None]).sum((0, 1)) + (p.shape[0] * p.shape[1] + 4) * 2.0 ** -24 * mass[-1])
+    return torch.from_numpy(lse).cuda(), mass, tol
+
+
+def _check(mass, before, want, tol, lens, what=""):
+    got, old = mass.double().cpu().numpy(), before.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        bound = tol[b] + 2.0 ** -24 * (np.abs(old[b, :n]) + want[b])
+        err = np.abs(got[b, :n] - old[b, :n] - want[b])
+        assert (err <= bound).all(), f"{what} request {b}: off by {err.max():.3e}, {(err / bound).max():.2f} of its bound"
+        assert (got[b, n:] == old[b, n:]).all()
+
+
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("lens,new,page,ratio", CASES)
+def test_attn_mass(csa2, lens, new, page, ratio, H):  # noqa: F811
+    case = _case(csa2, lens, new, H, page, ratio, seed=sum(lens) + H, pad=2)
+    cache, _, _, _, start, pos, q = case
+    lse, want, tol = _reference(case, lens, ratio, 1 / math.sqrt(512))
+    lse[-2:] = float("nan")                       # rows behind the last request are not read into anything
+    q[-2:] = float("nan")
+    before = torch.rand(cache.batch, cache.capacity, generator=torch.Generator().manual_seed(1)).cuda()
+    mass = before.clone()
+    csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(start).cuda(), ratio=ratio)
+    st, word = csa2.get_error(cache)
+    assert st == csa2.OK, word
+    _check(mass, before, want, tol, lens)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("lens", [[5000], [1] * 5 + [900] * 8, [30000, 20000]])
+def test_attn_mass_single_tokens(csa2, lens, H):  # noqa: F811
+    case = _case(csa2, lens, [1] * len(lens), H, 128, seed=len(lens))
+    cache, _, _, _, start, pos, q = case
+    lse, want, tol = _reference(case, lens, 1, 1 / math.sqrt(512))
+    mass = torch.zeros(cache.batch, cache.capacity, device="cuda")
+    p = torch.from_numpy(pos).cuda()
+    csa2.attn_mass(cache, q, p, lse, mass)
+    _check(mass, torch.zeros_like(mass), want, tol, lens)
+    again = csa2.attn_mass(cache, q, p, lse, torch.zeros_like(mass))
+    assert torch.equal(mass, again)
+
+
+@pytest.mark.parametrize("H,new", [(16, 300), (32, 129), (64, 700)])
+def test_attn_mass_positions_in_any_order(csa2, H, new):  # noqa: F811
+    """Shuffled positions (whole items that see nothing of a unit among them),
+    units cut over pairs and joined, a negative scale."""
+    lens = [777]
+    pos = np.random.default_rng(4).integers(-3, 900, new)
+    pos[: new // 2] %= 200
+    case = _case(csa2, lens, [new], H, 128, seed=9, pos=pos)
+    cache, _, _, _, start, p, q = case
+    lse, want, tol = _reference(case, lens, 1, -0.03)
+    mass = torch.zeros(1, cache.capacity, device="cuda")
+    csa2.attn_mass(cache, q, torch.from_numpy(p).cuda(), lse, mass, torch.from_numpy(start).cuda(), scale=-0.03)
+    _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
+def test_attn_mass_sums_to_the_queries(csa2):  # noqa: F811
+    """With chunk_attn's own lse the weights of a request sum to (queries that
+    see something) x H."""
+    lens, new, H = [2000, 333], [64, 333], 32
+    case = _case(csa2, lens, new, H, 128, seed=3)
+    cache, _, _, _, start, pos, q = case
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    lse = torch.empty(q.shape[:2], device="cuda")
+    csa2.chunk_attn(cache, q, p, s, lse=lse)
+    mass = csa2.attn_mass(cache, q, p, lse, torch.zeros(2, cache.capacity, device="cuda"), s)
+    total = mass.double().sum(1).cpu()
+    # both sides' scores are off by at most d each (see _reference): 1e-3 here
+    assert abs(float(total[0]) - 64 * H) < 2e-3 * 64 * H and abs(float(total[1]) - 333 * H) < 2e-3 * 333 * H
+
+
+def test_attn_mass_recorded_violations(csa2):  # noqa: F811
+    for what in ("page", "ctx", "start"):
+        lens, new, H = [300, 200], [70, 3], 32
+        case = _case(csa2, lens, new, H, 128, seed=5)
+        cache, _, _, _, start, pos, q = case
+        lse, want, tol = _reference(case, lens, 1, 1 / math.sqrt(512))
+        s = start.copy()
+        if what == "page":
+            cache.page_table[0, 1] = cache.num_pages
+        elif what == "ctx":
+            cache.ctx_len[0] = -7
+        else:
+            s[0] = -4
+        mass = torch.zeros(2, cache.capacity, device="cuda")
+        csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(s).cuda())
+        st, word = csa2.get_error(cache)
+        assert st == csa2.ERR_DEVICE_BOUNDS and word[2] == 0, (what, word)
+        if what == "page":
+            assert (mass[0, 128:256] == 0).all() and (mass[0, :128] > 0).all()
+        else:
+            assert (mass[0] == 0).all()
+        _check(mass[1:], torch.zeros_like(mass[1:]), want[1:], tol[1:], lens[1:])
+
+
+def test_attn_mass_graph(csa2):  # noqa: F811
+    lens, new, H = [700, 90], [33, 20], 32
+    case = _case(csa2, lens, new, H, 128, seed=15)
+    cache, _, _, _, start, pos, q = case
+    lse, want, tol = _reference(case, lens, 1, 1 / math.sqrt(512))
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    ws = torch.empty(csa2.attn_mass_workspace_bytes(cache, q.shape[0], H), dtype=torch.uint8, device="cuda")
+    mass = torch.zeros(2, cache.capacity, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        csa2.attn_mass(cache, q, p, lse, mass, s, workspace=ws)
+    mass.zero_()
+    ws.fill_(0xFF)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    _check(mass, torch.zeros_like(mass), [2 * w for w in want], [2 * t for t in tol], lens)
+
+
+def test_attn_mass_wait_limit(csa2):  # noqa: F811
+    """A wait that runs out is recorded and the launch ends; the next one is
+    unharmed."""
+    lens, new, H = [700], [300], 64
+    case = _case(csa2, lens, new, H, 128, seed=15)
+    cache, _, _, _, start, pos, q = case
+    lse, want, tol = _reference(case, lens, 1, 1 / math.sqrt(512))
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    mass = torch.zeros(1, cache.capacity, device="cuda")
+    csa2.set_wait_limit_ns(0)
+    try:
+        csa2.attn_mass(cache, q, p, lse, mass, s)
+        st, _ = csa2.get_error(cache)
+    finally:
+        csa2.set_wait_limit_ns(2_000_000_000)
+    assert st == csa2.ERR_TIMEOUT
+    cache.err_word.zero_()
+    mass.zero_()
+    csa2.attn_mass(cache, q, p, lse, mass, s)
+    st, word = csa2.get_error(cache)
+    assert st == csa2.OK, word
+    _check(mass, torch.zeros_like(mass), want, tol, lens)

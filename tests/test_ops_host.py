@@ -89,3 +89,18 @@ def test_chunk_attn_refusals(lib):  # noqa: F811
     assert call(size=need - 1) == lib.ERR_SHAPE
     assert b"csa2_chunk_attn_workspace_bytes" in lib._lib.csa2_last_error_message()
     assert call(n=0, pos=None, q=None, out=None, ws=None, size=0) == lib.OK
+
+
+def test_attn_mass_refusals(lib):  # noqa: F811
+    c, p = _cache(lib)
+    P, f = ctypes.c_void_p(p), lib._lib.csa2_attn_mass
+    need = lib._lib.csa2_attn_mass_workspace_bytes(2, 2, 64)
+    assert need > 0
+
+    def call(cache=c, n=2, start=P, pos=P, ratio=1, q=P, H=64, scale=0.1, lse=P, mass=P, ws=P, size=need):
+        return f(ctypes.byref(cache), n, start, pos, ratio, q, H, F32(scale), lse, mass, ws, size, None)
+    assert call(n=-1) == lib.ERR_SHAPE and call(n=3, start=None) == lib.ERR_SHAPE
+    assert call(ratio=0) == lib.ERR_SHAPE and call(H=8) == lib.ERR_SHAPE and call(scale=float("nan")) == lib.ERR_ARG
+    assert call(q=ctypes.c_void_p(p + 2)) == lib.ERR_ARG and call(lse=None) == lib.ERR_ARG and call(mass=None) == lib.ERR_ARG
+    assert call(ws=None) == lib.ERR_ARG and call(size=need - 1) == lib.ERR_SHAPE
+    assert call(n=0, pos=None, q=None, lse=None, mass=None, ws=None, size=0) == lib.OK

@@ -143,6 +143,39 @@ CSA2_API csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, 
                                     const float* lse, float* mass, void* workspace, size_t workspace_bytes,
                                     void* stream);
 
+/*
+ * csa2_evict -- keep `budget` entries of every longer request and move them to
+ * other pages.  Of a request's n = ctx_len entries the first `sink`, the last
+ * `recent` and, of those between, the (budget - sink - recent) with the largest
+ * mass are kept (ties: the lower index; a NaN counts as the largest, -0 as 0),
+ * in their old order: the new cache is the old one without the others.
+ * Requests with n <= budget are left where they are.
+ *   mass       float [batch][capacity] (from csa2_attn_mass)
+ *   budget     >= 1; sink, recent >= 0, sink + recent <= budget
+ *   dst_pages  int32 [batch][dst_width]: the pages that receive a request's
+ *              rows (dst_width * page_size >= budget; entries of requests that
+ *              are left alone are not read).  They must be free: a page that
+ *              holds visible entries of any request, or is given twice, is a
+ *              violation and receives nothing.  Pages that requests share
+ *              stay as they are.
+ *   kept       int32 [batch][budget] out: kept positions, ascending, -1 padded
+ *   new_len    int32 [batch] out: min(n, budget)
+ *   mass_out   float [batch][dst_width * page_size] or NULL: the kept entries'
+ *              mass (requests that are moved, their first `budget` values)
+ *   ik4        the FP4 indexer keys to move with the rows, or NULL
+ *   workspace  at least csa2_evict_workspace_bytes bytes, 16-byte aligned
+ * kept, new_len and mass_out overlap no input.  ctx_len and the page table are
+ * not modified: the caller continues with dst_pages and new_len for the
+ * requests that were moved and frees their old pages.
+ * Device errors: CSA2_ERR_DEVICE_BOUNDS for a bad page (the row is not moved)
+ * or ctx_len (the request counts as empty).
+ */
+CSA2_API size_t csa2_evict_workspace_bytes(int32_t num_pages);
+CSA2_API csa2_status csa2_evict(const csa2_cache* cache, const csa2_ik4* ik4, const float* mass, int32_t budget,
+                                int32_t sink, int32_t recent, const int32_t* dst_pages, int32_t dst_width,
+                                int32_t* kept, int32_t* new_len, float* mass_out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -72,6 +72,7 @@ _sig = {
     "csa2_norm_rope_append": [_CP, _KP, _I, _I, _P, _L, _P, _L, _P, _P, _F, _RP, _RP, _P, _P, _P, _P],
     "csa2_chunk_attn": [_CP, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, ctypes.c_size_t, _P],
     "csa2_attn_mass": [_CP, _I, _P, _P, _I, _P, _I, _F, _P, _P, _P, ctypes.c_size_t, _P],
+    "csa2_evict": [_CP, _KP, _P, _I, _I, _I, _P, _I, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "csa2_get_error": [_CP, ctypes.POINTER(ctypes.c_int32), _P],
 }
 for _name, _args in _sig.items():
@@ -91,6 +92,8 @@ _lib.csa2_chunk_attn_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.csa2_chunk_attn_workspace_bytes.restype = ctypes.c_size_t
 _lib.csa2_attn_mass_workspace_bytes.argtypes = [_I, _I, _I]
 _lib.csa2_attn_mass_workspace_bytes.restype = ctypes.c_size_t
+_lib.csa2_evict_workspace_bytes.argtypes = [_I]
+_lib.csa2_evict_workspace_bytes.restype = ctypes.c_size_t
 _lib.csa2_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
 _lib.csa2_set_wait_limit_ns.restype = None
 
@@ -631,6 +634,37 @@ def attn_mass(cache: Cache, q, q_pos, lse, mass, q_start=None, ratio: int = 1, s
                                    scale, _ptr(lse), _ptr(mass), _ptr(workspace), workspace.numel(), _stream(dev)),
                "csa2_attn_mass")
     return mass
+
+
+def evict_workspace_bytes(cache: Cache) -> int:
+    return int(_lib.csa2_evict_workspace_bytes(cache.num_pages))
+
+
+def evict(cache: Cache, mass, budget: int, dst_pages, sink: int = 0, recent: int = 0, kept=None, new_len=None,
+          mass_out=None, ik4: Ik4 | None = None, workspace=None):
+    """Keeps `budget` entries of every longer request by their mass float32
+    [batch, capacity] and moves their rows to dst_pages int32 [batch, pages]
+    (free pages); returns (kept int32 [batch, budget], new_len int32 [batch]).
+    mass_out: optional float32 [batch, pages * page_size], the kept entries'
+    mass.  The cache's page table and lengths are not changed."""
+    B, width = cache.batch, dst_pages.shape[1]
+    dev = cache.err_word.device
+    _arg(mass, torch.float32, (B, cache.capacity), "mass", dev)
+    _arg(dst_pages, torch.int32, (B, width), "dst_pages", dev)
+    if kept is None:
+        kept = torch.empty(B, max(int(budget), 0), dtype=torch.int32, device=dev)
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    _arg(kept, torch.int32, (B, budget), "kept", dev)
+    _arg(new_len, torch.int32, (B,), "new_len", dev)
+    _arg(mass_out, torch.float32, (B, width * cache.page_size), "mass_out", dev)
+    with torch.cuda.device(dev):
+        workspace = _workspace(workspace, evict_workspace_bytes(cache), dev)
+        _check(_lib.csa2_evict(ctypes.byref(cache.struct), None if ik4 is None else ctypes.byref(ik4.struct),
+                               _ptr(mass), int(budget), int(sink), int(recent), _ptr(dst_pages), width, _ptr(kept),
+                               _ptr(new_len), _ptr(mass_out), _ptr(workspace), workspace.numel(), _stream(dev)),
+               "csa2_evict")
+    return kept, new_len
 
 
 def get_error(cache: Cache):

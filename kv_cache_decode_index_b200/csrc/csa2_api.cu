@@ -683,6 +683,36 @@ csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, const int
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "attn_mass launch");
 }
 
+size_t csa2_evict_workspace_bytes(int32_t num_pages) {
+  return num_pages < 1 ? 0 : csa2::evict_workspace_bytes(num_pages);
+}
+
+csa2_status csa2_evict(const csa2_cache* cache, const csa2_ik4* ik4, const float* mass, int32_t budget, int32_t sink,
+                       int32_t recent, const int32_t* dst_pages, int32_t dst_width, int32_t* kept, int32_t* new_len,
+                       float* mass_out, void* workspace, size_t workspace_bytes, void* stream) {
+  CSA2_TRY(check_cache(cache, true, true));
+  if (ik4 != nullptr) CSA2_TRY(check_ik4(ik4));
+  if (budget < 1) return fail(CSA2_ERR_SHAPE, "budget %d < 1", budget);
+  if (sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > budget)
+    return fail(CSA2_ERR_SHAPE, "sink %d and recent %d must be >= 0 and together at most the budget (%d)", sink, recent, budget);
+  if (dst_width < 1 || static_cast<long long>(dst_width) * cache->page_size < budget)
+    return fail(CSA2_ERR_SHAPE, "dst_width %d pages hold fewer than budget (%d) rows", dst_width, budget);
+  if (static_cast<long long>(cache->batch) * budget >= (1LL << 31))
+    return fail(CSA2_ERR_SHAPE, "batch * budget must stay below 2^31");
+  if (mass == nullptr || dst_pages == nullptr || kept == nullptr || new_len == nullptr)
+    return fail(CSA2_ERR_ARG, "mass, dst_pages, kept and new_len must be set");
+  if (mass_out == mass) return fail(CSA2_ERR_ARG, "mass_out must not be mass");
+  if (new_len == cache->ctx_len) return fail(CSA2_ERR_ARG, "new_len must not be the cache's ctx_len");
+  if (dst_pages == cache->page_table) return fail(CSA2_ERR_ARG, "dst_pages must not be the cache's page table");
+  CSA2_TRY(check_workspace(workspace, workspace_bytes, csa2_evict_workspace_bytes(cache->num_pages),
+                           "csa2_evict_workspace_bytes"));
+  DeviceInfo d;
+  CSA2_TRY(device_info(&d));
+  const cudaError_t e = csa2::launch_evict(*cache, ik4, mass, budget, sink, recent, dst_pages, dst_width, kept, new_len,
+                                           mass_out, workspace, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "evict launch");
+}
+
 csa2_status csa2_get_error(const csa2_cache* cache, int32_t* out, void* stream) {
   if (cache == nullptr || cache->err_word == nullptr || out == nullptr)
     return fail(CSA2_ERR_ARG, "cache, cache.err_word and out must be set");

@@ -143,4 +143,10 @@ cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32
                              int ratio, int H, float scale, const float* lse, float* mass, void* ws,
                              const CUtensorMap& q_map, int num_sms, uint64_t wait_ns, cudaStream_t stream);
 
+// Eviction by weight: selection, then the kept rows to their new pages.
+size_t evict_workspace_bytes(long long num_pages);
+cudaError_t launch_evict(const csa2_cache& cache, const csa2_ik4* ik4, const float* mass, int budget, int sink, int recent,
+                         const int32_t* dst_pages, int dst_width, int32_t* kept, int32_t* new_len, float* mass_out,
+                         void* ws, cudaStream_t stream);
+
 }  // namespace csa2

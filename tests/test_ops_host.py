@@ -104,3 +104,22 @@ def test_attn_mass_refusals(lib):  # noqa: F811
     assert call(q=ctypes.c_void_p(p + 2)) == lib.ERR_ARG and call(lse=None) == lib.ERR_ARG and call(mass=None) == lib.ERR_ARG
     assert call(ws=None) == lib.ERR_ARG and call(size=need - 1) == lib.ERR_SHAPE
     assert call(n=0, pos=None, q=None, lse=None, mass=None, ws=None, size=0) == lib.OK
+
+
+def test_evict_refusals(lib):  # noqa: F811
+    c, p = _cache(lib)
+    P, f = ctypes.c_void_p(p), lib._lib.csa2_evict
+    Q, R = ctypes.c_void_p(p + 512), ctypes.c_void_p(p + 1024)
+    need = lib._lib.csa2_evict_workspace_bytes(4)
+    assert need == 16 and lib._lib.csa2_evict_workspace_bytes(0) == 0
+
+    def call(cache=c, ik4=None, mass=P, budget=100, sink=1, recent=9, dst=R, width=1, kept=Q, new_len=Q, out=None, ws=P,
+             size=need):
+        return f(ctypes.byref(cache), ik4, mass, budget, sink, recent, dst, width, kept, new_len, out, ws, size, None)
+    assert call(budget=0) == lib.ERR_SHAPE and call(sink=-1) == lib.ERR_SHAPE and call(recent=100) == lib.ERR_SHAPE
+    assert call(sink=2 ** 31 - 1, recent=2 ** 31 - 1) == lib.ERR_SHAPE
+    assert call(budget=129) == lib.ERR_SHAPE and call(width=0) == lib.ERR_SHAPE
+    assert call(mass=None) == lib.ERR_ARG and call(dst=None) == lib.ERR_ARG and call(kept=None) == lib.ERR_ARG
+    assert call(out=P) == lib.ERR_ARG and call(new_len=P) == lib.ERR_ARG and call(dst=P) == lib.ERR_ARG
+    assert call(ws=None) == lib.ERR_ARG and call(size=need - 1) == lib.ERR_SHAPE
+    assert call(ik4=ctypes.byref(lib.Ik4Struct(None, None))) == lib.ERR_ARG

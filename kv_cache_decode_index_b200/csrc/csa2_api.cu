@@ -655,7 +655,7 @@ csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries, const in
   DeviceInfo d;
   CSA2_TRY(device_info(&d));
   const cudaError_t e = csa2::launch_chunk_attn(*cache, n_queries, q_start, q_pos, ratio, q, H, scale, out, lse, workspace,
-                                                d.sms, static_cast<cudaStream_t>(stream));
+                                                d.sms, g_wait_limit_ns, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "chunk_attn launch");
 }
 

@@ -15,7 +15,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_tile.cuh"
-#include "dense_plan.cuh"
+#include "chunk_join.cuh"
 #include "launch.h"
 
 namespace csa2 {
@@ -25,25 +25,6 @@ namespace {
 constexpr int kCThreads = 256;
 constexpr int kCWarps = kCThreads / 32;
 constexpr int kDimsPerWarp = kKvDim / kCWarps;   // 64 output channels per warp in P V
-constexpr int kJoinParts = 8;                    // channel parts of a joined tile
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxCtas = 296;                    // ranges of one launch (two CTAs on each of 148 SMs)
-constexpr int kMaxRows = 64;
-constexpr size_t kPartialFloats = static_cast<size_t>(kMaxRows) * (kKvDim + 2);
-
-// Workspace: the CTAs' records, then two partial results per CTA (the tile
-// that a range starts inside, the tile that it ends inside).
-struct ChunkWorkspace {
-  RangeRecord* rec;
-  float* part;
-};
-__host__ __device__ inline ChunkWorkspace split_chunk_ws(void* ws) {
-  ChunkWorkspace w;
-  w.rec = static_cast<RangeRecord*>(ws);
-  w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMaxCtas * sizeof(RangeRecord));
-  return w;
-}
-
 template <int MR>
 struct ChunkSmem {
   static constexpr int HT = MR / 16;
@@ -76,17 +57,7 @@ __global__ void __launch_bounds__(kCThreads, MR == 16 ? 2 : 1)
   const ChunkWorkspace wsp = split_chunk_ws(ws);
 
   const DensePlan plan = dense_plan<kCThreads, kChunk>(a, S.plan, blockIdx.x, gridDim.x, kKChunk);
-  if (tid == 0) {
-    RangeRecord r = {plan.lo, plan.lo, plan.lo, 0, 0, plan.ctas, 0};
-    if (plan.lo < plan.hi) {
-      const DenseTile t = dense_tile(a, S.plan, plan.tile);
-      r.tile_lo = plan.lo - plan.off;
-      r.tile_hi = r.tile_lo + dense_steps<kChunk>(t);
-      r.q0 = t.q0;
-      r.tokens = t.tokens;
-    }
-    wsp.rec[blockIdx.x] = r;
-  }
+  if (tid == 0) write_range_record<kCThreads, kChunk>(a, S.plan, plan, &wsp.rec[blockIdx.x]);
 
   const int r0 = lane >> 2;
   const int h0 = ht * 16 + r0, h1 = h0 + 8;
@@ -347,7 +318,7 @@ __global__ void __launch_bounds__(kCThreads, MR == 16 ? 2 : 1)
             lse[orow] = l == 0.0f ? -INFINITY : (m_run[t][hf] + log2f(l)) * kLn2;
         }
     } else {
-      float* part = wsp.part + (2 * static_cast<size_t>(blockIdx.x) + (off > 0 ? 0 : 1)) * kPartialFloats;
+      float* part = partial_of(wsp, blockIdx.x, off > 0 ? 0 : 1, MR);
 #pragma unroll
       for (int t = 0; t < L::HT; ++t)
 #pragma unroll
@@ -359,53 +330,54 @@ __global__ void __launch_bounds__(kCThreads, MR == 16 ? 2 : 1)
           for (int i = 0; i < kDimsPerWarp / 8; ++i)
             *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o_acc[t][i][2 * hf], o_acc[t][i][2 * hf + 1]);
           if (warp == 0 && (lane & 3) == 0) {
-            part[kMaxRows * kKvDim + row] = m_run[t][hf];
-            part[kMaxRows * (kKvDim + 1) + row] = l_run[t][hf];
+            part[MR * kKvDim + row] = m_run[t][hf];
+            part[MR * (kKvDim + 1) + row] = l_run[t][hf];
           }
         }
     }
   }
 }
 
-// Joins the tiles that ranges cut: block (c, part) takes the tile that range c
-// starts inside, if c is the first to do so, and 64 of its channels.
-__global__ void __launch_bounds__(kCThreads)
-    chunk_join_kernel(int heads, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, void* ws) {
+// Joins the tiles that ranges cut: block (c, y) takes rows 4y .. 4y + 3 of the
+// tile that range c starts inside, if c is the first to do so; 128 threads
+// take four channels each of a row.
+constexpr int kJoinRows = 4;
+
+__global__ void __launch_bounds__(kJoinRows * kKvDim / 4)
+    chunk_join_kernel(int heads, int tile_rows, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, void* ws) {
   const ChunkWorkspace wsp = split_chunk_ws(ws);
-  const int c = blockIdx.x, ch0 = blockIdx.y * (kKvDim / kJoinParts);
+  const int c = blockIdx.x;
   const RangeRecord r = wsp.rec[c];
   if (c >= r.ctas || r.lo == r.tile_lo || wsp.rec[c - 1].lo > r.tile_lo) return;
+  const int row = blockIdx.y * kJoinRows + threadIdx.x / (kKvDim / 4), d = (threadIdx.x % (kKvDim / 4)) * 4;
+  if (row >= r.tokens * heads) return;
   int last = c;
   while (last + 1 < r.ctas && wsp.rec[last + 1].lo < r.tile_hi) ++last;
-  const int rows = r.tokens * heads;
-  // the tile's head came from range c - 1: its last tile, or its first when it starts with it
-  for (int i = threadIdx.x; i < rows * (kKvDim / kJoinParts / 4); i += kCThreads) {
-    const int row = i / (kKvDim / kJoinParts / 4), d = ch0 + (i % (kKvDim / kJoinParts / 4)) * 4;
-    float M = -INFINITY;
-    for (int k = c - 1; k <= last; ++k)
-      M = fmaxf(M, wsp.part[(2 * static_cast<size_t>(k) + (k < c ? 1 : 0)) * kPartialFloats + kMaxRows * kKvDim + row]);
-    const float ref = M == -INFINITY ? 0.0f : M;
-    float l = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = c - 1; k <= last; ++k) {
-      const float* part = wsp.part + (2 * static_cast<size_t>(k) + (k < c ? 1 : 0)) * kPartialFloats;
-      const float f = exp2f(part[kMaxRows * kKvDim + row] - ref);
-      l = fmaf(part[kMaxRows * (kKvDim + 1) + row], f, l);
-      const float4 v = *reinterpret_cast<const float4*>(part + row * kKvDim + d);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    const long long orow = static_cast<long long>(r.q0) * heads + row;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    uint2 pk;
-    pk.x = *reinterpret_cast<const uint32_t*>(&lo);
-    pk.y = *reinterpret_cast<const uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(out + orow * kKvDim + d) = pk;
-    if (lse != nullptr && d == 0) lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
+  // the tile's head came from range c - 1, which ended (or also began) with it
+  float M = -INFINITY;
+  for (int k = c - 1; k <= last; ++k) M = fmaxf(M, partial_of(wsp, k, k < c ? 1 : 0, tile_rows)[tile_rows * kKvDim + row]);
+  const float ref = M == -INFINITY ? 0.0f : M;
+  float l = 0.0f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = c - 1; k <= last; ++k) {
+    const float* part = partial_of(wsp, k, k < c ? 1 : 0, tile_rows);
+    const float f = exp2f(part[tile_rows * kKvDim + row] - ref);
+    l = fmaf(part[tile_rows * (kKvDim + 1) + row], f, l);
+    const float4 v = *reinterpret_cast<const float4*>(part + row * kKvDim + d);
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
   }
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+  const long long orow = static_cast<long long>(r.q0) * heads + row;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  uint2 pk;
+  pk.x = *reinterpret_cast<const uint32_t*>(&lo);
+  pk.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(out + orow * kKvDim + d) = pk;
+  if (lse != nullptr && d == 0) lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 template <int MR>
@@ -418,30 +390,40 @@ cudaError_t launch_chunk(const DenseArgs& a, const uint16_t* q, float scale, uin
                                 static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
-  const int ctas = min(kMaxCtas, num_sms * (MR == 16 ? 2 : 1));
+  const int ctas = min(kMaxRanges, num_sms * (MR == 16 ? 2 : 1));
   chunk_attn_kernel<MR><<<ctas, kCThreads, smem, stream>>>(a, reinterpret_cast<const __nv_bfloat16*>(q), scale,
                                                            reinterpret_cast<__nv_bfloat16*>(out), lse, ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  chunk_join_kernel<<<dim3(ctas, kJoinParts), kCThreads, 0, stream>>>(a.heads, reinterpret_cast<__nv_bfloat16*>(out), lse,
-                                                                      ws);
-  return cudaGetLastError();
+  return launch_chunk_join(a.heads, MR, ctas, out, lse, ws, stream);
 }
 
 }  // namespace
 
+cudaError_t launch_chunk_join(int heads, int tile_rows, int ranges, uint16_t* out, float* lse, void* ws,
+                              cudaStream_t stream) {
+  chunk_join_kernel<<<dim3(ranges, (tile_rows + kJoinRows - 1) / kJoinRows), kJoinRows * kKvDim / 4, 0, stream>>>(
+      heads, tile_rows, reinterpret_cast<__nv_bfloat16*>(out), lse, ws);
+  return cudaGetLastError();
+}
+
 size_t chunk_attn_workspace_bytes() {
-  return kMaxCtas * sizeof(RangeRecord) + 2 * static_cast<size_t>(kMaxCtas) * kPartialFloats * sizeof(float);
+  return kMaxRanges * sizeof(RangeRecord) + static_cast<size_t>(kWsRows) * (kKvDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_chunk_attn(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
                               int ratio, const uint16_t* q, int H, float scale, uint16_t* out, float* lse, void* ws,
-                              int num_sms, cudaStream_t stream) {
+                              int num_sms, uint64_t wait_ns, cudaStream_t stream) {
   DenseArgs a = {cache, q_start, q_pos, n_queries, ratio, H, 1, 2};
+  if (true) {
+    a.tile_tokens = 128 / H;
+    a.min_steps = 1;
+    return launch_chunk_attn_pair(a, q, scale, out, lse, ws, num_sms, wait_ns, stream);
+  }
   // One token per tile while requests have about one each; more tokens share a
   // tile of 64 rows otherwise.
   const bool single = n_queries <= cache.batch;
-  a.tile_tokens = single ? 1 : kMaxRows / H;
+  a.tile_tokens = single ? 1 : 64 / H;
   switch (a.tile_tokens * H) {
     case 16: return launch_chunk<16>(a, q, scale, out, lse, ws, num_sms, stream);
     case 32: return launch_chunk<32>(a, q, scale, out, lse, ws, num_sms, stream);

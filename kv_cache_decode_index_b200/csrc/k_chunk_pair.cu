@@ -1,0 +1,579 @@
+// csa2_chunk_attn on the tensor cores of a pair of CTAs: 128 query rows (64
+// per CTA) over the keys in tiles of 256.
+//
+//   S = Q K^T   M = 128 rows, N = 256 keys, K = 512 channels (8 parts of 64)
+//   O += P V    M = 128 rows, N = 2 x 256 channels, K = 256 keys (8 parts of 32)
+//
+// Both products take the dequantised row as operand B, once with the channels
+// as K (K-major) and once with the keys as K (MN-major).  tcgen05 over a pair
+// has each CTA hold one half of B's N: its 128 keys of the tile for S, its 256
+// channels of every key for O.  Why a pair with M = 128: 512 output channels of
+// 128 rows in fp32 are a whole SM's tensor memory; over a pair they take half
+// of each (256 columns), which leaves room for two score tiles (2 x 128), and
+// N = 256 keeps the full rate that M = 128 has over a pair (64 cycles per MMA
+// of K = 16; N = 128 takes 47, no less than N = 64).
+//
+// Roles: warps 0-3 softmax (thread = row and half of the tile's keys), warps
+// 4-11 dequantisation (packed rows from L2 into registers one half tile ahead,
+// fp16 operands into a ring of 16 KB slots), warp 12 of the leader issues the
+// MMAs in the order S(0), S(1), O(0), S(2), O(1), ...: the softmax of a tile has
+// the time of the next tile's S and of the previous tile's O.
+//
+// The rows are stored times 2^-8 (an E4M3 code shifted into fp16 is 2^-8 of its
+// value; the product with E2M1 stays exact in fp16, subnormals included);
+// the scores' factor and the output's carry the 2^8.
+// The running maximum is raised only when a row's new maximum is more than 2^8
+// above it (the probabilities stay below 2^8 until then, well inside fp16), so
+// that O, which lies in tensor memory, is rarely rescaled.
+#include <cuda_bf16.h>
+
+#include "attn_tile.cuh"
+#include "chunk_join.cuh"
+#include "cta_pair.cuh"
+#include "dense_plan.cuh"
+#include "launch.h"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kGSoftWarps = 4, kGDeqWarps = 8;
+constexpr int kGThreads = (kGSoftWarps + kGDeqWarps + 1) * 32;   // 416
+constexpr int kGKeys = 256;                  // keys of a tile
+constexpr int kGRows = 64;                   // query rows of one CTA
+constexpr int kGSlots = 7;
+constexpr int kSlotBytes = 16384;
+constexpr uint32_t kGTmemCols = 512;
+constexpr uint32_t kOCol = 0, kSCol = 256;   // O: 2 x 128 columns; S: 2 buffers of 128
+constexpr uint32_t kIdescS = idesc_f16_f32(128, 256, false, false);
+constexpr uint32_t kIdescO = idesc_f16_f32(128, 256, false, true);
+constexpr int kBarSoft = 1;
+constexpr float kRaise = 8.0f;               // log2 units a maximum may rise before O is rescaled
+constexpr float kFar = 1048576.0f;           // 2^20: fp32 values are less than 1/8 apart below it
+constexpr float kRowScale = 256.0f;          // stored rows are 2^-8 of their value
+
+struct __align__(1024) PairSmem {
+  uint8_t q[8][kGRows * 128];                // A of S: 64-channel parts
+  uint8_t p[4][kGRows * 128];                // A of O: 64-key parts
+  uint8_t slot[kGSlots][kSlotBytes];
+  float xchg[2][128];
+  float row_scale[kGRows];
+  int row_lim[kGRows];
+  uint64_t slot_full[kGSlots];               // leader: both CTAs' dequantisation
+  uint64_t slot_empty[kGSlots];
+  uint64_t s_full[2];
+  uint64_t p_full;                           // leader: both CTAs' softmax
+  uint64_t o_done;
+  uint64_t q_full;                           // leader
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  DensePlanSmem<kGThreads> plan;
+};
+static_assert(sizeof(PairSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of an MN-major operand with the 128-byte swizzle: 64 elements of
+// N contiguous per K row (128 bytes), 8-row groups 1024 bytes apart, the next
+// 64 elements of N `atom` bytes on.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t atom) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(atom >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// 32 channels of a packed row (16 code bytes, two scale codes in the low half
+// of `sc`) -> four 16-byte chunks of fp16, each value times 2^-8.  Any scale
+// byte gives finite values (rows that nobody sees may hold any).
+__device__ __forceinline__ void dequant_32(uint4 codes, uint32_t sc, uint4 (&out)[4]) {
+  const uint32_t b0 = (sc & 0x7Fu) << 7, b1 = ((sc >> 8) & 0x7Fu) << 7;
+  const uint32_t s0 = b0 | (b0 << 16), s1 = b1 | (b1 << 16);
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w[i]));
+    const uint32_t s = i < 2 ? s0 : s1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), *reinterpret_cast<const __half2*>(&s));
+      h[k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    out[i] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+// One half tile of a dequantising thread: the packed bytes of its 8 slots.
+struct HalfTile {
+  uint4 codes[8];
+  uint32_t sc[8];
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
+    chunk_attn_pair_kernel(const DenseArgs a, const __nv_bfloat16* __restrict__ q, float scale,
+                           __nv_bfloat16* __restrict__ out, float* __restrict__ lse, void* ws, uint64_t wait_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  PairSmem& S = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1;
+  const csa2_cache& cache = a.cache;
+  const ChunkWorkspace wsp = split_chunk_ws(ws);
+
+  if (tid == 0) {
+    for (int s = 0; s < kGSlots; ++s) {
+      mbar_init(&S.slot_full[s], 4);             // two warps of each CTA
+      mbar_init(&S.slot_empty[s], 1);
+    }
+    mbar_init(&S.s_full[0], 1);
+    mbar_init(&S.s_full[1], 1);
+    mbar_init(&S.p_full, 2 * kGSoftWarps);
+    mbar_init(&S.o_done, 1);
+    mbar_init(&S.q_full, 2 * kGSoftWarps);
+    mbar_init(&S.drain, 1);
+    S.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) tmem_alloc_pair(&S.tmem_base, kGTmemCols);
+  const DensePlan plan = dense_plan<kGThreads, kGKeys>(a, S.plan, pair, gridDim.x >> 1, kKChunk);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync_all();
+  const uint32_t tmem = S.tmem_base;
+  if (tid == 0 && rank == 0) write_range_record<kGThreads, kGKeys>(a, S.plan, plan, &wsp.rec[pair]);
+
+  if (warp < kGSoftWarps) {
+    // ================= softmax =================
+    const int row = tid & 63, khalf = tid >> 6;      // row of this CTA, keys khalf*128 .. +127 of the tile
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t p_full = map_rank(smem_u32(&S.p_full), 0), q_full = map_rank(smem_u32(&S.q_full), 0);
+    const float sign = scale < 0.0f ? -1.0f : 1.0f;
+    int g = 0;                                       // tiles so far
+    bool ok = true;
+    long long pos = plan.lo;
+    int off = plan.off;
+    for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0) {
+      const DenseTile T = dense_tile(a, S.plan, ti);
+      const int steps = dense_steps<kGKeys>(T);
+      const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
+      pos += seg;
+      const int rows = T.tokens * a.heads;           // of the pair
+      // queries -> fp16 with a power-of-two scale per row (as bf16 they are kept whole)
+      for (int r = warp; r < kGRows; r += kGSoftWarps) {
+        const int pr = static_cast<int>(rank) * kGRows + r;
+        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+        if (pr < rows) {
+          const uint4* src =
+              reinterpret_cast<const uint4*>(q + (static_cast<long long>(T.q0) * a.heads + pr) * kKvDim) + lane * 2;
+          v0 = src[0];
+          v1 = src[1];
+        }
+        const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        float f[16], amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[2 * i] = __uint_as_float(wv[i] << 16);
+          f[2 * i + 1] = __uint_as_float(wv[i] & 0xFFFF0000u);
+          amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        int E = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 127;
+        if (amax == 0.0f) E = 14;
+        E = max(E, -100);
+        const float up = exp2i(14 - E) * sign, down = exp2i(E - 14);
+        uint32_t hv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) hv[i] = pack_half2(f[2 * i] * up, f[2 * i + 1] * up);
+        // lane: channels 16*lane .. +15: part lane / 4, chunks 2*(lane % 4), +1
+        uint8_t* dst = S.q[lane >> 2] + r * 128;
+        const int c0 = 2 * (lane & 3);
+        *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+        if (lane == 0) {
+          S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
+          S.row_lim[r] = pr < rows ? seen_by(a.q_pos[T.q0 + pr / a.heads], a.ratio, S.plan.ctx[T.b]) : 0;
+        }
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(kBarSoft, kGSoftWarps * 32);
+      if (lane == 0) mbar_arrive_cluster(q_full);
+      const float c2 = S.row_scale[row];
+      const int lim = S.row_lim[row];
+      float m_ref = -INFINITY, l = 0.0f;
+
+      for (int t = 0; t < seg; ++t, ++g) {
+        const int key0 = (off + t) * kGKeys + khalf * 128;
+        const uint32_t s_addr = tmem + lane_base + kSCol + (g & 1) * 128;
+        if (!mbar_wait_warp(&S.s_full[g & 1], (g >> 1) & 1, wait_ns)) ok = false;
+        ok = !named_bar_or(kBarSoft, kGSoftWarps * 32, !ok || S.abort_flag != 0);
+        if (!ok) break;
+        tc_fence_after();
+        const bool masked = __any_sync(0xffffffffu, lim < key0 + 128);
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(s_addr + c, r);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (key0 + c + j < lim) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
+          }
+        }
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+        S.xchg[g & 1][tid] = mx;
+        named_bar_sync(kBarSoft, kGSoftWarps * 32);
+        mx = fmaxf(mx, S.xchg[g & 1][tid ^ 64]);
+        const float m_new = mx == -INFINITY ? -INFINITY : mx * c2;
+        float f = 1.0f;
+        if (m_new > m_ref + kRaise || (m_ref == -INFINITY && m_new != -INFINITY)) {
+          f = m_ref == -INFINITY ? 0.0f : ex2(m_ref - m_new);
+          m_ref = m_new;
+          l *= f;
+        }
+        const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
+        // far from 0, s * c2 - ref has to be rounded like ref was
+        const bool careful = __any_sync(0xffffffffu, lim < key0 + 128 || !(fabsf(ref) < kFar));
+        // P and O of the previous tile are free once its product is done
+        if (g > 0 && t > 0) {
+          if (!mbar_wait_warp(&S.o_done, (g - 1) & 1, wait_ns)) ok = false;
+          tc_fence_after();
+          if (ok && __any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+            for (int c = 0; c < 256; c += 32) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+              tmem_st_32x32b_x32(tmem + lane_base + kOCol + c, r);
+            }
+            tmem_st_wait();
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(s_addr + c, r);
+          tmem_ld_wait();
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint32_t h[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float s0 = __uint_as_float(r[j]), s1 = __uint_as_float(r[j + 1]);
+            float p0, p1;
+            if (careful) {
+              p0 = key0 + c + j < lim ? ex2(__fsub_rn(__fmul_rn(s0, c2), ref)) : 0.0f;
+              p1 = key0 + c + j + 1 < lim ? ex2(__fsub_rn(__fmul_rn(s1, c2), ref)) : 0.0f;
+            } else {
+              p0 = ex2(fmaf(s0, c2, -ref));
+              p1 = ex2(fmaf(s1, c2, -ref));
+            }
+            sum[(j >> 1) & 3] += p0 + p1;
+            h[j >> 1] = pack_half2(p0, p1);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          uint8_t* dst = S.p[khalf * 2 + (c >> 6)] + row * 128;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + (((((c & 32) >> 3) + j) ^ (row & 7)) << 4)) =
+                make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
+      }
+      if (!ok) break;
+      // ---- the segment's rows ----
+      ok = mbar_wait_warp(&S.o_done, (g - 1) & 1, wait_ns);
+      ok = !named_bar_or(kBarSoft, kGSoftWarps * 32, !ok);
+      if (!ok) break;
+      tc_fence_after();
+      S.xchg[g & 1][tid] = l;
+      named_bar_sync(kBarSoft, kGSoftWarps * 32);
+      l = S.xchg[g & 1][row] + S.xchg[g & 1][row + 64];
+      const int pr = static_cast<int>(rank) * kGRows + row;
+      const bool whole = seg == steps;
+      const float inv = whole ? (l > 0.0f ? kRowScale / l : (l == 0.0f ? 0.0f : l)) : kRowScale;
+      const long long orow = static_cast<long long>(T.q0) * a.heads + pr;
+      float* part = partial_of(wsp, pair, off > 0 ? 0 : 1, 2 * kGRows);
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
+        tmem_ld_wait();
+        // column c of the lane: channel (c / 128) * 256 + khalf * 128 + c % 128
+        const int ch = (c >> 7) * 256 + khalf * 128 + (c & 127);
+        if (pr < rows) {
+          if (whole) {
+            uint32_t h[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const __nv_bfloat162 b =
+                  __floats2bfloat162_rn(__uint_as_float(r[2 * j]) * inv, __uint_as_float(r[2 * j + 1]) * inv);
+              h[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(out + orow * kKvDim + ch);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[j] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(part + pr * kKvDim + ch);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
+                                   __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
+          }
+        }
+      }
+      if (khalf == 0 && pr < rows) {
+        if (!whole) {
+          part[2 * kGRows * kKvDim + pr] = m_ref;
+          part[2 * kGRows * (kKvDim + 1) + pr] = l;
+        } else if (lse != nullptr) {
+          lse[orow] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(kBarSoft, kGSoftWarps * 32);    // Q, the row tables and O are free
+    }
+    if (!ok) {
+      if (lane == 0) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, static_cast<int>(rank), g);
+      S.abort_flag = 1;
+    }
+  } else if (warp < kGSoftWarps + kGDeqWarps) {
+    // ================= dequantisation =================
+    // Two warps fill a slot, so four slots are under way at once: group
+    // q takes slots q and q + 4 of every half tile (8 slots).  A lane's four
+    // granules of a slot (32 channels of a key each): K: keys krow + 32 i, one
+    // 32-channel half of the slot's 64; V: keys vkey + 8 i of the slot's 32, one
+    // 32-channel part of this CTA's 256.  Eight neighbouring lanes hold eight
+    // neighbouring keys: their 16-byte stores fall into different banks.
+    const int dw = warp - kGSoftWarps, q4 = dw >> 1, d64 = (dw & 1) * 32 + lane;
+    const int krow = (d64 >> 4) * 8 + (lane & 7), kg = (lane >> 3) & 1;
+    const int vkey = lane & 7, vg = d64 >> 3;
+    const int v_code = (vg >> 2) * 128 + static_cast<int>(rank) * 64 + (vg & 3) * 16;
+    const int v_sc = (vg >> 2) * 16 + static_cast<int>(rank) * 8 + (vg & 3) * 2;
+    const uint32_t k_dst = krow * 128, v_dst = ((vg >> 2) * 2 + ((vg & 3) >> 1)) * 4096 + vkey * 128;
+    const int k_c = kg * 4, v_c = (vg & 1) * 4;
+
+    // first cache row of the 128 keys from `key` on, or -1: not seen by the tile, or a bad page
+    auto block_row = [&](const DenseTile& T, int key) {
+      if (key >= T.keys) return -1;
+      const int page = cache.page_table[static_cast<long long>(T.b) * cache.max_pages_per_req + key / cache.page_size];
+      if (page < 0 || page >= cache.num_pages) {
+        report_error(cache.err_word, CSA2_ERR_DEVICE_BOUNDS, kKChunk, T.b, key);
+        return -1;
+      }
+      return page * cache.page_size + key % cache.page_size;
+    };
+    auto load_k = [&](const DenseTile& T, int tile, HalfTile& h) {
+      const int base = block_row(T, tile * kGKeys + static_cast<int>(rank) * 128);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {                  // slot q4 + 4 (i / 4), key krow + 32 (i % 4)
+        const int c = q4 + (i >> 2) * 4;
+        h.codes[i] = make_uint4(0, 0, 0, 0);
+        h.sc[i] = 0;
+        if (base >= 0) {
+          const long long r = base + krow + (i & 3) * 32;
+          h.codes[i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + c * 32 + kg * 16);
+          h.sc[i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + c * 4 + kg * 2);
+        }
+      }
+    };
+    auto load_v = [&](const DenseTile& T, int tile, HalfTile& h) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {                  // slot q4 + 4 b: keys 32 (q4 + 4 b) + vkey + 8 i
+        const int base = block_row(T, tile * kGKeys + b * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h.codes[b * 4 + i] = make_uint4(0, 0, 0, 0);
+          h.sc[b * 4 + i] = 0;
+          if (base >= 0) {
+            const long long r = base + q4 * 32 + vkey + i * 8;
+            h.codes[b * 4 + i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + v_code);
+            h.sc[b * 4 + i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + v_sc);
+          }
+        }
+      }
+    };
+    int n = q4;                                      // this group's next slot in the order of all slots
+    bool ok = true;
+    // step: bytes from one of the lane's four keys to the next
+    auto store = [&](const HalfTile& h, uint32_t dst_off, uint32_t step, int chunk0, int x) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b, n += 4) {
+        const int s = n % kGSlots;
+        if (ok && (S.abort_flag || !mbar_wait_warp(&S.slot_empty[s], ((n / kGSlots) & 1) ^ 1, wait_ns))) ok = false;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 o[4];
+          dequant_32(h.codes[b * 4 + i], h.sc[b * 4 + i], o);
+          uint8_t* dst = S.slot[s] + dst_off + i * step;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((chunk0 + j) ^ x) << 4)) = o[j];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.slot_full[s]), 0));
+      }
+    };
+
+    long long pos = plan.lo;
+    int off = plan.off;
+    HalfTile cur, nxt;
+    // the order of the MMAs: K(0), then K(t), V(t - 1), and V of the last tile
+    if (pos < plan.hi) load_k(dense_tile(a, S.plan, plan.tile), off, cur);
+    for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0) {
+      const DenseTile T = dense_tile(a, S.plan, ti);
+      const int steps = dense_steps<kGKeys>(T);
+      const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
+      pos += seg;
+      for (int t = 0; ok && t < seg; ++t) {
+        // cur holds K(t)
+        if (t > 0) load_v(T, off + t - 1, nxt);
+        else if (seg > 1) load_k(T, off + 1, nxt);
+        else load_v(T, off, nxt);
+        store(cur, k_dst, 32 * 128, k_c, krow & 7);
+        cur = nxt;
+        if (t == 0) continue;                        // cur: K(1), or V(0) of a segment of one tile
+        // cur holds V(t - 1)
+        if (t + 1 < seg) load_k(T, off + t + 1, nxt);
+        else load_v(T, off + t, nxt);
+        store(cur, v_dst, 8 * 128, v_c, vkey & 7);
+        cur = nxt;
+      }
+      // cur holds V(seg - 1)
+      if (pos < plan.hi) load_k(dense_tile(a, S.plan, ti + 1), 0, nxt);
+      if (ok) store(cur, v_dst, 8 * 128, v_c, vkey & 7);
+      cur = nxt;
+    }
+    if (!ok && lane == 0) {
+      report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, static_cast<int>(rank), -n);
+      S.abort_flag = 1;
+    }
+  } else if (rank == 0) {
+    // ================= MMA issuer =================
+    if (lane == 0) {
+      int n = 0, g = 0, segs = 0;
+      bool ok = true;
+      auto slot = [&]() {
+        const int s = n % kGSlots;
+        if (S.abort_flag || !mbar_wait_cluster(&S.slot_full[s], (n / kGSlots) & 1, wait_ns)) ok = false;
+        tc_fence_after();
+        return s;
+      };
+      auto scores = [&](int buf) {
+        for (int c = 0; c < 8; ++c, ++n) {
+          const int s = slot();
+          if (!ok) return;
+          const uint64_t ad = sw128_kmajor_desc(smem_u32(S.q[c])), bd = sw128_kmajor_desc(smem_u32(S.slot[s]));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_pair(tmem + kSCol + buf * 128, ad + 2 * kk, bd + 2 * kk, kIdescS, (c | kk) > 0 ? 1u : 0u);
+          umma_commit_pair(&S.slot_empty[s]);
+        }
+        umma_commit_pair(&S.s_full[buf]);
+      };
+      auto output = [&](int tile, bool first) {      // tile: running number
+        if (!mbar_wait_cluster(&S.p_full, tile & 1, wait_ns)) ok = false;
+        tc_fence_after();
+        for (int j = 0; ok && j < 8; ++j, ++n) {
+          const int s = slot();
+          if (!ok) return;
+          const uint64_t ad = sw128_kmajor_desc(smem_u32(S.p[j >> 1])) + (j & 1) * 4;
+          const uint32_t b = smem_u32(S.slot[s]);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              umma_f16_pair(tmem + kOCol + x * 128, ad + 2 * kk, sw128_mnmajor_desc(b + kk * 2048 + x * 8192, 4096), kIdescO,
+                            first && (j | kk) == 0 ? 0u : 1u);
+          umma_commit_pair(&S.slot_empty[s]);
+        }
+        if (ok) umma_commit_pair(&S.o_done);
+      };
+      long long pos = plan.lo;
+      int off = plan.off;
+      for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0, ++segs) {
+        const int steps = dense_steps<kGKeys>(dense_tile(a, S.plan, ti));
+        const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
+        pos += seg;
+        if (!mbar_wait_cluster(&S.q_full, segs & 1, wait_ns)) ok = false;
+        tc_fence_after();
+        for (int t = 0; ok && t < seg; ++t, ++g) {
+          scores(g & 1);
+          if (ok && t > 0) output(g - 1, t == 1);
+        }
+        if (ok) output(g - 1, seg == 1);
+      }
+      if (!ok) {
+        report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, -1, g);
+        S.abort_flag = 1;
+      }
+      umma_commit_pair(&S.drain);
+      (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
+    }
+  } else {
+    if (lane == 0) (void)mbar_wait(&S.drain, 0, 4 * kWaitLimitNs);   // the leader's last arrival here
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();          // every MMA has completed, no barrier of the other CTA is touched after this
+  if (warp == 12) tmem_release_pair(tmem, kGTmemCols);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attn_pair(const DenseArgs& a, const uint16_t* q, float scale, uint16_t* out, float* lse, void* ws,
+                                   int num_sms, uint64_t wait_ns, cudaStream_t stream) {
+  static ContextMemo attrs;
+  const size_t smem = sizeof(PairSmem) + 1024;
+  cudaError_t e = attrs.once([&] {
+    return cudaFuncSetAttribute(chunk_attn_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem));
+  });
+  if (e != cudaSuccess) return e;
+  const int pairs = min(kMaxRanges / 2, num_sms / 2);   // twice the rows per range
+  chunk_attn_pair_kernel<<<2 * pairs, kGThreads, smem, stream>>>(a, reinterpret_cast<const __nv_bfloat16*>(q), scale,
+                                                                 reinterpret_cast<__nv_bfloat16*>(out), lse, ws, wait_ns);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_chunk_join(a.heads, a.tile_tokens * a.heads, pairs, out, lse, ws, stream);
+}
+
+}  // namespace csa2

@@ -136,7 +136,7 @@ cudaError_t launch_norm_rope_append(const csa2_cache& cache, const csa2_ik4* ik4
 size_t chunk_attn_workspace_bytes();
 cudaError_t launch_chunk_attn(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
                               int ratio, const uint16_t* q, int H, float scale, uint16_t* out, float* lse, void* ws,
-                              int num_sms, cudaStream_t stream);
+                              int num_sms, uint64_t wait_ns, cudaStream_t stream);
 // Attention weight of every entry; q_map: the query rows in boxes of 32 rows x 64 channels.
 size_t attn_mass_workspace_bytes();
 cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,

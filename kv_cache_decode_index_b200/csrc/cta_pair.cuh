@@ -51,6 +51,26 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same wait by every lane of a warp, the outcome as a vote: the warp stays
+// converged and the compiler sees that it does.
+__device__ __forceinline__ bool mbar_wait_cluster_all(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit_ns)) != 0;
+}
+
+// True in one lane of a converged warp.  The warp that issues MMAs runs its
+// loop in all lanes and issues under this predicate: descriptors then stay in
+// uniform registers.  Under `if (lane == 0)` every MMA took about 180 cycles to
+// issue, of the 64 that it takes to run.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)), "r"(ncols)
                : "memory");

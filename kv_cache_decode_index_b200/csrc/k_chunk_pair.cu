@@ -487,66 +487,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     }
   } else if (rank == 0) {
     // ================= MMA issuer =================
-    if (lane == 0) {
-      int n = 0, g = 0, segs = 0;
-      bool ok = true;
-      auto slot = [&]() {
-        const int s = n % kGSlots;
-        if (S.abort_flag || !mbar_wait_cluster(&S.slot_full[s], (n / kGSlots) & 1, wait_ns)) ok = false;
-        tc_fence_after();
-        return s;
-      };
-      auto scores = [&](int buf) {
-        for (int c = 0; c < 8; ++c, ++n) {
-          const int s = slot();
-          if (!ok) return;
-          const uint64_t ad = sw128_kmajor_desc(smem_u32(S.q[c])), bd = sw128_kmajor_desc(smem_u32(S.slot[s]));
+    const bool issue = elect_one();
+    const uint64_t q_desc = sw128_kmajor_desc(smem_u32(S.q[0])), p_desc = sw128_kmajor_desc(smem_u32(S.p[0]));
+    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.slot[0]));
+    const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(S.slot[0]), 4096);
+    int s = 0, g = 0, segs = 0;                      // slot in turn and its phase
+    uint32_t phase = 0;
+    bool ok = true;
+    auto slot_ready = [&]() {
+      ok = S.abort_flag == 0 && mbar_wait_cluster_all(&S.slot_full[s], phase, wait_ns);
+      ok = __all_sync(0xffffffffu, ok) != 0;
+      tc_fence_after();
+    };
+    auto next_slot = [&]() {
+      if (++s == kGSlots) {
+        s = 0;
+        phase ^= 1;
+      }
+    };
+    auto scores = [&](int buf) {
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        slot_ready();
+        if (!ok) return;
+        if (issue) {
+          const uint64_t ad = q_desc + c * (kGRows * 128 / 16), bd = k_desc + s * (kSlotBytes / 16);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_f16_pair(tmem + kSCol + buf * 128, ad + 2 * kk, bd + 2 * kk, kIdescS, (c | kk) > 0 ? 1u : 0u);
           umma_commit_pair(&S.slot_empty[s]);
+          if (c == 7) umma_commit_pair(&S.s_full[buf]);
         }
-        umma_commit_pair(&S.s_full[buf]);
-      };
-      auto output = [&](int tile, bool first) {      // tile: running number
-        if (!mbar_wait_cluster(&S.p_full, tile & 1, wait_ns)) ok = false;
-        tc_fence_after();
-        for (int j = 0; ok && j < 8; ++j, ++n) {
-          const int s = slot();
-          if (!ok) return;
-          const uint64_t ad = sw128_kmajor_desc(smem_u32(S.p[j >> 1])) + (j & 1) * 4;
-          const uint32_t b = smem_u32(S.slot[s]);
+        __syncwarp();
+        next_slot();
+      }
+    };
+    auto output = [&](int tile, bool first) {        // tile: running number
+      ok = mbar_wait_cluster_all(&S.p_full, tile & 1, wait_ns);
+      tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; ok && j < 8; ++j) {
+        slot_ready();
+        if (!ok) return;
+        if (issue) {
+          const uint64_t ad = p_desc + (j >> 1) * (kGRows * 128 / 16) + (j & 1) * 4;
+          const uint64_t bd = v_desc + s * (kSlotBytes / 16);
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              umma_f16_pair(tmem + kOCol + x * 128, ad + 2 * kk, sw128_mnmajor_desc(b + kk * 2048 + x * 8192, 4096), kIdescO,
+              umma_f16_pair(tmem + kOCol + x * 128, ad + 2 * kk, bd + kk * (2048 / 16) + x * (8192 / 16), kIdescO,
                             first && (j | kk) == 0 ? 0u : 1u);
           umma_commit_pair(&S.slot_empty[s]);
+          if (j == 7) umma_commit_pair(&S.o_done);
         }
-        if (ok) umma_commit_pair(&S.o_done);
-      };
-      long long pos = plan.lo;
-      int off = plan.off;
-      for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0, ++segs) {
-        const int steps = dense_steps<kGKeys>(dense_tile(a, S.plan, ti));
-        const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
-        pos += seg;
-        if (!mbar_wait_cluster(&S.q_full, segs & 1, wait_ns)) ok = false;
-        tc_fence_after();
-        for (int t = 0; ok && t < seg; ++t, ++g) {
-          scores(g & 1);
-          if (ok && t > 0) output(g - 1, t == 1);
-        }
-        if (ok) output(g - 1, seg == 1);
+        __syncwarp();
+        next_slot();
       }
-      if (!ok) {
-        report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, -1, g);
-        S.abort_flag = 1;
+    };
+    long long pos = plan.lo;
+    int off = plan.off;
+    for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0, ++segs) {
+      const int steps = dense_steps<kGKeys>(dense_tile(a, S.plan, ti));
+      const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
+      pos += seg;
+      ok = mbar_wait_cluster_all(&S.q_full, segs & 1, wait_ns);
+      tc_fence_after();
+      for (int t = 0; ok && t < seg; ++t, ++g) {
+        scores(g & 1);
+        if (ok && t > 0) output(g - 1, t == 1);
       }
-      umma_commit_pair(&S.drain);
-      (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
+      if (ok) output(g - 1, seg == 1);
     }
+    if (lane == 0 && !ok) {
+      report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, -1, g);
+      S.abort_flag = 1;
+    }
+    __syncwarp();
+    if (issue) umma_commit_pair(&S.drain);           // the lane that issued: its commits track its own operations
+    (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
   } else {
     if (lane == 0) (void)mbar_wait(&S.drain, 0, 4 * kWaitLimitNs);   // the leader's last arrival here
   }

@@ -230,52 +230,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
         (void)mbar_wait(&S.full[j % kMStages], (j / kMStages) & 1, kWaitLimitNs / 2);
   } else if (warp == 1 && rank == 0) {
     // ================= MMA issuer =================
-    int i = 0, item = 0, units = 0, b = 0;      // units: those with an item that is computed
+    const bool issue = elect_one();
+    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.k[0])), q_desc = sw128_kmajor_desc(smem_u32(S.q[0]));
+    int s = 0, item = 0, units = 0, b = 0;      // units: those with an item that is computed
+    uint32_t phase = 0;
     bool ok = true;
     for (long long pos = lo; ok && pos < hi;) {
       const Unit u = unit_at(pos, b);
       b = u.b;
       pos += u.t1 - u.t0;
       bool loaded = false;
-      for (int t = u.t0; t < u.t1; ++t) {
+      for (int t = u.t0; ok && t < u.t1; ++t) {
         if (!tile_seen(u, t)) continue;
         if (!loaded) {
-          if (lane == 0 && ok) ok = mbar_wait_cluster(&S.k_full, units & 1, wait_ns);
+          ok = mbar_wait_cluster_all(&S.k_full, units & 1, wait_ns);
           loaded = true;
           ++units;
         }
         const uint32_t idesc = idesc_f16_f32(kMKeys, columns(u, t), true, false);
-        if (lane == 0 && ok) {
-          const int acc = item % kMAcc;
-          ok = mbar_wait_cluster(&S.acc_empty[acc], ((item / kMAcc) & 1) ^ 1, wait_ns);
+        const int acc = item % kMAcc;
+        ok = mbar_wait_cluster_all(&S.acc_empty[acc], ((item / kMAcc) & 1) ^ 1, wait_ns) && ok;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; ok && c < kKvDim / 64; ++c) {
+          ok = __all_sync(0xffffffffu, S.abort_flag == 0 && mbar_wait(&S.full[s], phase, wait_ns)) != 0;
+          if (!ok) break;
           tc_fence_after();
-          for (int c = 0; ok && c < kKvDim / 64; ++c, ++i) {
-            const int s = i % kMStages;
-            if (S.abort_flag || !mbar_wait(&S.full[s], (i / kMStages) & 1, wait_ns)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t ad = sw128_kmajor_desc(smem_u32(S.k[c])), bd = sw128_kmajor_desc(smem_u32(S.q[s]));
+          if (issue) {
+            const uint64_t ad = k_desc + c * (kAtomBytes / 16), bd = q_desc + s * (kAtomBytes / 16);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_f16_pair(tmem + acc * kMRows, ad + 2 * kk, bd + 2 * kk, idesc, (c | kk) > 0 ? 1u : 0u);
             umma_commit_pair(&S.empty[s]);
+            if (c == kKvDim / 64 - 1) umma_commit_pair(&S.acc_full[acc]);
           }
-          if (ok) umma_commit_pair(&S.acc_full[acc]);
+          __syncwarp();
+          if (++s == kMStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
         ++item;
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     }
     if (lane == 0 && !ok) {
       report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, -1, item);
       S.abort_flag = 1;
     }
-    if (lane == 0) {
-      umma_commit_pair(&S.drain);
-      (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
-    }
+    __syncwarp();
+    if (issue) umma_commit_pair(&S.drain);
+    (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
   } else if (warp == 1) {
     if (lane == 0) (void)mbar_wait(&S.drain, 0, 2 * kWaitLimitNs);   // the leader's last arrival here
   } else {

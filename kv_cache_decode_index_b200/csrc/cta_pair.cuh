@@ -23,10 +23,13 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// Arrive on a barrier of either CTA (address from map_rank), releasing this
-// thread's earlier writes to the cluster.
+// Arrive on a barrier of either CTA (address from map_rank).  It announces
+// operands that this CTA wrote to its OWN shared memory, where its own tensor
+// core reads them: the writers' fence.proxy.async and the arrival's release at
+// CTA scope order those writes.  A release to the cluster would add nothing but
+// a wait for every load that the SM has in flight (about 1,000 cycles here).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // mbar_try_wait that acquires what the other CTA released.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {

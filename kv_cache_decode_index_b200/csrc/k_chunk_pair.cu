@@ -7,7 +7,7 @@
 // Both products take the dequantised row as operand B, once with the channels
 // as K (K-major) and once with the keys as K (MN-major).  tcgen05 over a pair
 // has each CTA hold one half of B's N: its 128 keys of the tile for S, its 256
-// channels of every key for O.  Why a pair with M = 128: 512 output channels of
+// neighbouring channels of every key for O.  Why a pair with M = 128: 512 output channels of
 // 128 rows in fp32 are a whole SM's tensor memory; over a pair they take half
 // of each (256 columns), which leaves room for two score tiles (2 x 128), and
 // N = 256 keeps the full rate that M = 128 has over a pair (64 cycles per MMA
@@ -332,8 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         uint32_t r[32];
         tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
         tmem_ld_wait();
-        // column c of the lane: channel (c / 128) * 256 + khalf * 128 + c % 128
-        const int ch = (c >> 7) * 256 + khalf * 128 + (c & 127);
+        const int ch = khalf * 256 + c;              // the upper lanes hold the other CTA's channels
         if (pr < rows) {
           if (whole) {
             uint32_t h[16];
@@ -372,18 +371,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     }
   } else if (warp < kGSoftWarps + kGDeqWarps) {
     // ================= dequantisation =================
-    // Two warps fill a slot, so four slots are under way at once: group
-    // q takes slots q and q + 4 of every half tile (8 slots).  A lane's four
-    // granules of a slot (32 channels of a key each): K: keys krow + 32 i, one
-    // 32-channel half of the slot's 64; V: keys vkey + 8 i of the slot's 32, one
-    // 32-channel part of this CTA's 256.  Eight neighbouring lanes hold eight
-    // neighbouring keys: their 16-byte stores fall into different banks.
-    const int dw = warp - kGSoftWarps, q4 = dw >> 1, d64 = (dw & 1) * 32 + lane;
-    const int krow = (d64 >> 4) * 8 + (lane & 7), kg = (lane >> 3) & 1;
-    const int vkey = lane & 7, vg = d64 >> 3;
-    const int v_code = (vg >> 2) * 128 + static_cast<int>(rank) * 64 + (vg & 3) * 16;
-    const int v_sc = (vg >> 2) * 16 + static_cast<int>(rank) * 8 + (vg & 3) * 2;
-    const uint32_t k_dst = krow * 128, v_dst = ((vg >> 2) * 2 + ((vg & 3) >> 1)) * 4096 + vkey * 128;
+    // Two warps fill two slots at a time, so that all groups' slots are under
+    // way at once: group q4 takes slots 2 q4 and 2 q4 + 1 of every half tile (8
+    // slots).  A granule is 32 channels of a key (16 code bytes).  A warp's load
+    // takes 8 keys x 64 bytes for K, 4 keys x 128 bytes for V (this CTA's
+    // channels are 256 neighbours): few cache lines an instruction, which the
+    // L1 looks up one by one.  A quarter warp holds 4 keys x 2 neighbouring
+    // granules: its 16-byte stores fall into eight different chunks.
+    const int dw = warp - kGSoftWarps, q4 = dw >> 1, wi = dw & 1;
+    // K: keys krow + 16 i, granule kg of slot 2 q4 + ksel
+    const int krow = wi * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), kg = (lane >> 2) & 1, ksel = lane >> 4;
+    // V: keys vkey + 8 i of the two slots' 64, granule vg of this CTA's 8
+    const int vkey = wi * 4 + (lane & 3), vg = (lane >> 3) * 2 + ((lane >> 2) & 1);
+    const int k_code = (2 * q4 + ksel) * 32 + kg * 16, k_sc = (2 * q4 + ksel) * 4 + kg * 2;
+    const int v_code = static_cast<int>(rank) * 128 + vg * 16, v_sc = static_cast<int>(rank) * 16 + vg * 2;
+    const uint32_t k_dst = krow * 128, v_dst = (vg >> 1) * 4096 + vkey * 128;
     const int k_c = kg * 4, v_c = (vg & 1) * 4;
 
     // first cache row of the 128 keys from `key` on, or -1: not seen by the tile, or a bad page
@@ -399,57 +401,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     auto load_k = [&](const DenseTile& T, int tile, HalfTile& h) {
       const int base = block_row(T, tile * kGKeys + static_cast<int>(rank) * 128);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {                  // slot q4 + 4 (i / 4), key krow + 32 (i % 4)
-        const int c = q4 + (i >> 2) * 4;
+      for (int i = 0; i < 8; ++i) {
         h.codes[i] = make_uint4(0, 0, 0, 0);
         h.sc[i] = 0;
         if (base >= 0) {
-          const long long r = base + krow + (i & 3) * 32;
-          h.codes[i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + c * 32 + kg * 16);
-          h.sc[i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + c * 4 + kg * 2);
+          const long long r = base + krow + i * 16;
+          h.codes[i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + k_code);
+          h.sc[i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + k_sc);
         }
       }
     };
     auto load_v = [&](const DenseTile& T, int tile, HalfTile& h) {
+      const int base = block_row(T, tile * kGKeys + (q4 >> 1) * 128);   // the slots' 64 keys lie in one block
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {                  // slot q4 + 4 b: keys 32 (q4 + 4 b) + vkey + 8 i
-        const int base = block_row(T, tile * kGKeys + b * 128);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h.codes[b * 4 + i] = make_uint4(0, 0, 0, 0);
-          h.sc[b * 4 + i] = 0;
-          if (base >= 0) {
-            const long long r = base + q4 * 32 + vkey + i * 8;
-            h.codes[b * 4 + i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + v_code);
-            h.sc[b * 4 + i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + v_sc);
-          }
+      for (int i = 0; i < 8; ++i) {
+        h.codes[i] = make_uint4(0, 0, 0, 0);
+        h.sc[i] = 0;
+        if (base >= 0) {
+          const long long r = base + (q4 & 1) * 64 + vkey + i * 8;
+          h.codes[i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + v_code);
+          h.sc[i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + v_sc);
         }
       }
     };
-    int n = q4;                                      // this group's next slot in the order of all slots
+    int n = 2 * q4;                                  // this group's next slot in the order of all slots
     bool ok = true;
-    // step: bytes from one of the lane's four keys to the next
-    auto store = [&](const HalfTile& h, uint32_t dst_off, uint32_t step, int chunk0, int x) {
+    auto wait_empty = [&](int slot_no) {
+      if (ok && (S.abort_flag || !mbar_wait(&S.slot_empty[slot_no % kGSlots], ((slot_no / kGSlots) & 1) ^ 1, wait_ns)))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto arrive_full = [&](int slot_no) {
+      if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.slot_full[slot_no % kGSlots]), 0));
+    };
+    auto put = [&](const HalfTile& h, int i, uint8_t* dst, int chunk0, int x) {
+      uint4 o[4];
+      dequant_32(h.codes[i], h.sc[i], o);
 #pragma unroll
-      for (int b = 0; b < 2; ++b, n += 4) {
-        const int s = n % kGSlots;
-        if (ok && (S.abort_flag || !mbar_wait_warp(&S.slot_empty[s], ((n / kGSlots) & 1) ^ 1, wait_ns))) ok = false;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          continue;
-        }
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((chunk0 + j) ^ x) << 4)) = o[j];
+    };
+    auto store_k = [&](const HalfTile& h) {          // both slots together: half a warp's lanes fill each
+      wait_empty(n);
+      wait_empty(n + 1);
+      if (ok) {
+        uint8_t* dst = S.slot[(n + ksel) % kGSlots] + k_dst;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 o[4];
-          dequant_32(h.codes[b * 4 + i], h.sc[b * 4 + i], o);
-          uint8_t* dst = S.slot[s] + dst_off + i * step;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((chunk0 + j) ^ x) << 4)) = o[j];
-        }
+        for (int i = 0; i < 8; ++i) put(h, i, dst + i * 16 * 128, k_c, krow & 7);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.slot_full[s]), 0));
+        arrive_full(n);
+        arrive_full(n + 1);
       }
+      n += 8;
+    };
+    auto store_v = [&](const HalfTile& h) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        wait_empty(n + b);
+        if (ok) {
+          uint8_t* dst = S.slot[(n + b) % kGSlots] + v_dst;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put(h, b * 4 + i, dst + i * 8 * 128, v_c, vkey & 7);
+          fence_proxy_async_smem();
+          __syncwarp();
+          arrive_full(n + b);
+        }
+      }
+      n += 8;
     };
 
     long long pos = plan.lo;
@@ -467,18 +485,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (t > 0) load_v(T, off + t - 1, nxt);
         else if (seg > 1) load_k(T, off + 1, nxt);
         else load_v(T, off, nxt);
-        store(cur, k_dst, 32 * 128, k_c, krow & 7);
+        store_k(cur);
         cur = nxt;
         if (t == 0) continue;                        // cur: K(1), or V(0) of a segment of one tile
         // cur holds V(t - 1)
         if (t + 1 < seg) load_k(T, off + t + 1, nxt);
         else load_v(T, off + t, nxt);
-        store(cur, v_dst, 8 * 128, v_c, vkey & 7);
+        store_v(cur);
         cur = nxt;
       }
       // cur holds V(seg - 1)
       if (pos < plan.hi) load_k(dense_tile(a, S.plan, ti + 1), 0, nxt);
-      if (ok) store(cur, v_dst, 8 * 128, v_c, vkey & 7);
+      if (ok) store_v(cur);
       cur = nxt;
     }
     if (!ok && lane == 0) {

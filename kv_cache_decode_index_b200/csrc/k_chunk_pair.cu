@@ -72,16 +72,22 @@ struct __align__(1024) PairSmem {
 };
 static_assert(sizeof(PairSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
+}
+// 32 lanes x 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -125,12 +131,6 @@ __device__ __forceinline__ void dequant_32(uint4 codes, uint32_t sc, uint4 (&out
     out[i] = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
-
-// One half tile of a dequantising thread: the packed bytes of its 8 slots.
-struct HalfTile {
-  uint4 codes[8];
-  uint32_t sc[8];
-};
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     chunk_attn_pair_kernel(const DenseArgs a, const __nv_bfloat16* __restrict__ q, float scale,
@@ -234,19 +234,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const bool masked = __any_sync(0xffffffffu, lim < key0 + 128);
+        // tensor-memory loads run one part ahead of the arithmetic
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(s_addr + c, r);
-          tmem_ld_wait();
-          if (masked) {
+        {
+          uint32_t r[2][32];
+          tmem_ld_32x32b_x32(s_addr, r[0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (key0 + c + j < lim) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
-          } else {
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld_32x32b_x32(s_addr + (c + 1) * 32, r[(c + 1) & 1]);
+            if (masked) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[j]));
+              for (int j = 0; j < 32; ++j)
+                if (key0 + c * 32 + j < lim) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[c & 1][j]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(r[c & 1][j]));
+            }
           }
         }
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
@@ -263,51 +267,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
         // far from 0, s * c2 - ref has to be rounded like ref was
         const bool careful = __any_sync(0xffffffffu, lim < key0 + 128 || !(fabsf(ref) < kFar));
+        // the probabilities wait in registers (fp16) for the previous tile's P to be free
+        uint32_t h[64];
+        {
+          uint32_t r[2][16];
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          tmem_ld_32x32b_x16(s_addr, r[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            tmem_ld_wait();
+            if (c < 7) tmem_ld_32x32b_x16(s_addr + (c + 1) * 16, r[(c + 1) & 1]);
+            if (careful) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const int key = key0 + c * 16 + j;
+                const float s0 = __uint_as_float(r[c & 1][j]), s1 = __uint_as_float(r[c & 1][j + 1]);
+                const float p0 = key < lim ? ex2(__fsub_rn(__fmul_rn(s0, c2), ref)) : 0.0f;
+                const float p1 = key + 1 < lim ? ex2(__fsub_rn(__fmul_rn(s1, c2), ref)) : 0.0f;
+                sum[(j >> 1) & 3] += p0 + p1;
+                h[c * 8 + (j >> 1)] = pack_half2(p0, p1);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float p0 = ex2(fmaf(__uint_as_float(r[c & 1][j]), c2, -ref));
+                const float p1 = ex2(fmaf(__uint_as_float(r[c & 1][j + 1]), c2, -ref));
+                sum[(j >> 1) & 3] += p0 + p1;
+                h[c * 8 + (j >> 1)] = pack_half2(p0, p1);
+              }
+            }
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
         // P and O of the previous tile are free once its product is done
-        if (g > 0 && t > 0) {
+        if (t > 0) {
           if (!mbar_wait_warp(&S.o_done, (g - 1) & 1, wait_ns)) ok = false;
           tc_fence_after();
           if (ok && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
-              uint32_t r[32];
-              tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
+            for (int c = 0; c < 256; c += 16) {
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(tmem + lane_base + kOCol + c, r);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
-              tmem_st_32x32b_x32(tmem + lane_base + kOCol + c, r);
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * f);
+              tmem_st_32x32b_x16(tmem + lane_base + kOCol + c, r);
             }
             tmem_st_wait();
           }
         }
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(s_addr + c, r);
-          tmem_ld_wait();
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          uint32_t h[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float s0 = __uint_as_float(r[j]), s1 = __uint_as_float(r[j + 1]);
-            float p0, p1;
-            if (careful) {
-              p0 = key0 + c + j < lim ? ex2(__fsub_rn(__fmul_rn(s0, c2), ref)) : 0.0f;
-              p1 = key0 + c + j + 1 < lim ? ex2(__fsub_rn(__fmul_rn(s1, c2), ref)) : 0.0f;
-            } else {
-              p0 = ex2(fmaf(s0, c2, -ref));
-              p1 = ex2(fmaf(s1, c2, -ref));
-            }
-            sum[(j >> 1) & 3] += p0 + p1;
-            h[j >> 1] = pack_half2(p0, p1);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          uint8_t* dst = S.p[khalf * 2 + (c >> 6)] + row * 128;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(dst + (((((c & 32) >> 3) + j) ^ (row & 7)) << 4)) =
-                make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-        }
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<uint4*>(S.p[khalf * 2 + (j >> 3)] + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
+              make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -398,30 +410,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       }
       return page * cache.page_size + key % cache.page_size;
     };
-    auto load_k = [&](const DenseTile& T, int tile, HalfTile& h) {
-      const int base = block_row(T, tile * kGKeys + static_cast<int>(rank) * 128);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h.codes[i] = make_uint4(0, 0, 0, 0);
-        h.sc[i] = 0;
-        if (base >= 0) {
-          const long long r = base + krow + i * 16;
-          h.codes[i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + k_code);
-          h.sc[i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + k_sc);
-        }
-      }
+    // Where a lane's 8 granules of a half tile lie: the first one's codes and
+    // scales, and the keys between two of them; no codes: zeros.
+    struct Half {
+      const uint8_t *codes, *scales;
+      int step;
     };
-    auto load_v = [&](const DenseTile& T, int tile, HalfTile& h) {
+    auto half_k = [&](const DenseTile& T, int tile) {
+      const int base = block_row(T, tile * kGKeys + static_cast<int>(rank) * 128);
+      const long long r = base + krow;
+      return Half{base < 0 ? nullptr : cache.kv_codes + r * kKvCodeBytes + k_code, cache.kv_scales + r * kKvScaleBytes + k_sc,
+                  16};
+    };
+    auto half_v = [&](const DenseTile& T, int tile) {
       const int base = block_row(T, tile * kGKeys + (q4 >> 1) * 128);   // the slots' 64 keys lie in one block
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h.codes[i] = make_uint4(0, 0, 0, 0);
-        h.sc[i] = 0;
-        if (base >= 0) {
-          const long long r = base + (q4 & 1) * 64 + vkey + i * 8;
-          h.codes[i] = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + v_code);
-          h.sc[i] = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + v_sc);
-        }
+      const long long r = base + (q4 & 1) * 64 + vkey;
+      return Half{base < 0 ? nullptr : cache.kv_codes + r * kKvCodeBytes + v_code, cache.kv_scales + r * kKvScaleBytes + v_sc,
+                  8};
+    };
+    uint4 codes[8];                                  // the lane's granules of the half tile in turn
+    uint32_t sc[8];
+    auto load = [&](const Half& h, int i) {
+      codes[i] = make_uint4(0, 0, 0, 0);
+      sc[i] = 0;
+      if (h.codes != nullptr) {
+        codes[i] = *reinterpret_cast<const uint4*>(h.codes + i * h.step * kKvCodeBytes);
+        sc[i] = *reinterpret_cast<const uint16_t*>(h.scales + i * h.step * kKvScaleBytes);
       }
     };
     int n = 2 * q4;                                  // this group's next slot in the order of all slots
@@ -434,19 +448,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     auto arrive_full = [&](int slot_no) {
       if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.slot_full[slot_no % kGSlots]), 0));
     };
-    auto put = [&](const HalfTile& h, int i, uint8_t* dst, int chunk0, int x) {
+    // granule i into a slot; its registers then receive that of the half tile after
+    auto put = [&](int i, uint8_t* dst, int chunk0, int x, const Half& next) {
       uint4 o[4];
-      dequant_32(h.codes[i], h.sc[i], o);
+      dequant_32(codes[i], sc[i], o);
 #pragma unroll
       for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((chunk0 + j) ^ x) << 4)) = o[j];
+      load(next, i);
     };
-    auto store_k = [&](const HalfTile& h) {          // both slots together: half a warp's lanes fill each
+    auto store_k = [&](const Half& next) {           // both slots together: half a warp's lanes fill each
       wait_empty(n);
       wait_empty(n + 1);
       if (ok) {
         uint8_t* dst = S.slot[(n + ksel) % kGSlots] + k_dst;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) put(h, i, dst + i * 16 * 128, k_c, krow & 7);
+        for (int i = 0; i < 8; ++i) put(i, dst + i * 16 * 128, k_c, krow & 7, next);
         fence_proxy_async_smem();
         __syncwarp();
         arrive_full(n);
@@ -454,14 +470,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       }
       n += 8;
     };
-    auto store_v = [&](const HalfTile& h) {
+    auto store_v = [&](const Half& next) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         wait_empty(n + b);
         if (ok) {
           uint8_t* dst = S.slot[(n + b) % kGSlots] + v_dst;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) put(h, b * 4 + i, dst + i * 8 * 128, v_c, vkey & 7);
+          for (int i = 0; i < 4; ++i) put(b * 4 + i, dst + i * 8 * 128, v_c, vkey & 7, next);
           fence_proxy_async_smem();
           __syncwarp();
           arrive_full(n + b);
@@ -472,32 +488,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
     long long pos = plan.lo;
     int off = plan.off;
-    HalfTile cur, nxt;
     // the order of the MMAs: K(0), then K(t), V(t - 1), and V of the last tile
-    if (pos < plan.hi) load_k(dense_tile(a, S.plan, plan.tile), off, cur);
+    if (pos < plan.hi) {
+      const Half first = half_k(dense_tile(a, S.plan, plan.tile), off);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load(first, i);
+    }
     for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0) {
       const DenseTile T = dense_tile(a, S.plan, ti);
       const int steps = dense_steps<kGKeys>(T);
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
       for (int t = 0; ok && t < seg; ++t) {
-        // cur holds K(t)
-        if (t > 0) load_v(T, off + t - 1, nxt);
-        else if (seg > 1) load_k(T, off + 1, nxt);
-        else load_v(T, off, nxt);
-        store_k(cur);
-        cur = nxt;
-        if (t == 0) continue;                        // cur: K(1), or V(0) of a segment of one tile
-        // cur holds V(t - 1)
-        if (t + 1 < seg) load_k(T, off + t + 1, nxt);
-        else load_v(T, off + t, nxt);
-        store_v(cur);
-        cur = nxt;
+        store_k(t > 0 ? half_v(T, off + t - 1) : (seg > 1 ? half_k(T, off + 1) : half_v(T, off)));
+        if (t > 0) store_v(t + 1 < seg ? half_k(T, off + t + 1) : half_v(T, off + t));
       }
-      // cur holds V(seg - 1)
-      if (pos < plan.hi) load_k(dense_tile(a, S.plan, ti + 1), 0, nxt);
-      if (ok) store_v(cur);
-      cur = nxt;
+      store_v(pos < plan.hi ? half_k(dense_tile(a, S.plan, ti + 1), 0) : Half{nullptr, nullptr, 0});
     }
     if (!ok && lane == 0) {
       report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, static_cast<int>(rank), -n);

@@ -26,6 +26,7 @@
 // above it (the probabilities stay below 2^8 until then, well inside fp16), so
 // that O, which lies in tensor memory, is rarely rescaled.
 #include <cuda_bf16.h>
+#include <stddef.h>
 
 #include "attn_tile.cuh"
 #include "chunk_join.cuh"
@@ -49,6 +50,7 @@ constexpr uint32_t kIdescS = idesc_f16_f32(128, 256, false, false);
 constexpr uint32_t kIdescO = idesc_f16_f32(128, 256, false, true);
 constexpr int kBarSoft = 1;
 constexpr float kRaise = 8.0f;               // log2 units a maximum may rise before O is rescaled
+constexpr int kStageRow = kKvDim * 2 + 16;     // bytes between staged output rows
 constexpr float kFar = 1048576.0f;           // 2^20: fp32 values are less than 1/8 apart below it
 constexpr float kRowScale = 256.0f;          // stored rows are 2^-8 of their value
 
@@ -70,6 +72,8 @@ struct __align__(1024) PairSmem {
   volatile int abort_flag;
   DensePlanSmem<kGThreads> plan;
 };
+static_assert(sizeof(PairSmem::q) + sizeof(PairSmem::p) >= kGRows * kStageRow, "staged output rows");
+static_assert(offsetof(PairSmem, p) == sizeof(PairSmem::q), "P lies behind Q");
 static_assert(sizeof(PairSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -91,6 +95,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Bulk copy of a row from shared to global memory (16-byte aligned, a multiple
+// of 16 bytes), and the wait for the thread's copies to have read their source.
+__device__ __forceinline__ void bulk_store_1d(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // Descriptor of an MN-major operand with the 128-byte swizzle: 64 elements of
 // N contiguous per K row (128 bytes), 8-row groups 1024 bytes apart, the next
 // 64 elements of N `atom` bytes on.
@@ -104,11 +117,11 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint3
   return d;
 }
 
-// 32 channels of a packed row (16 code bytes, two scale codes in the low half
-// of `sc`) -> four 16-byte chunks of fp16, each value times 2^-8.  Any scale
-// byte gives finite values (rows that nobody sees may hold any).
+// 32 channels of a packed row (16 code bytes, two scale codes below 0x80 in the
+// low half of `sc`) -> four 16-byte chunks of fp16, each value times 2^-8.  Any
+// scale code gives finite values (rows that nobody sees may hold any bytes).
 __device__ __forceinline__ void dequant_32(uint4 codes, uint32_t sc, uint4 (&out)[4]) {
-  const uint32_t b0 = (sc & 0x7Fu) << 7, b1 = ((sc >> 8) & 0x7Fu) << 7;
+  const uint32_t b0 = (sc & 0xFFu) << 7, b1 = (sc >> 8) << 7;
   const uint32_t s0 = b0 | (b0 << 16), s1 = b1 | (b1 << 16);
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
@@ -145,7 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kGSlots; ++s) {
-      mbar_init(&S.slot_full[s], 4);             // two warps of each CTA
+      mbar_init(&S.slot_full[s], 8);             // four warps of each CTA
       mbar_init(&S.slot_empty[s], 1);
     }
     mbar_init(&S.s_full[0], 1);
@@ -182,41 +195,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
       const int rows = T.tokens * a.heads;           // of the pair
-      // queries -> fp16 with a power-of-two scale per row (as bf16 they are kept whole)
-      for (int r = warp; r < kGRows; r += kGSoftWarps) {
-        const int pr = static_cast<int>(rank) * kGRows + r;
-        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-        if (pr < rows) {
-          const uint4* src =
-              reinterpret_cast<const uint4*>(q + (static_cast<long long>(T.q0) * a.heads + pr) * kKvDim) + lane * 2;
-          v0 = src[0];
-          v1 = src[1];
-        }
-        const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-        float f[16], amax = 0.0f;
+      // queries -> fp16 with a power-of-two scale per row (as bf16 they are
+      // kept whole), eight rows' loads in flight
+#pragma unroll 1
+      for (int r0 = warp; r0 < kGRows; r0 += 8 * kGSoftWarps) {
+        uint4 v[8][2];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          f[2 * i] = __uint_as_float(wv[i] << 16);
-          f[2 * i + 1] = __uint_as_float(wv[i] & 0xFFFF0000u);
-          amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+          const int pr = static_cast<int>(rank) * kGRows + r0 + i * kGSoftWarps;
+          v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+          if (pr < rows) {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(q + (static_cast<long long>(T.q0) * a.heads + pr) * kKvDim) + lane * 2;
+            v[i][0] = src[0];
+            v[i][1] = src[1];
+          }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        int E = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFF) - 127;
-        if (amax == 0.0f) E = 14;
-        E = max(E, -100);
-        const float up = exp2i(14 - E) * sign, down = exp2i(E - 14);
-        uint32_t hv[8];
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i * kGSoftWarps, pr = static_cast<int>(rank) * kGRows + r;
+          const uint32_t wv[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+          uint32_t top = 0;                          // exponent and mantissa of the largest magnitude (bf16 bits order like it)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) hv[i] = pack_half2(f[2 * i] * up, f[2 * i + 1] * up);
-        // lane: channels 16*lane .. +15: part lane / 4, chunks 2*(lane % 4), +1
-        uint8_t* dst = S.q[lane >> 2] + r * 128;
-        const int c0 = 2 * (lane & 3);
-        *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-        *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-        if (lane == 0) {
-          S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
-          S.row_lim[r] = pr < rows ? seen_by(a.q_pos[T.q0 + pr / a.heads], a.ratio, S.plan.ctx[T.b]) : 0;
+          for (int k = 0; k < 8; ++k) top = max(top, max(wv[k] & 0x7FFFu, (wv[k] >> 16) & 0x7FFFu));
+          top = __reduce_max_sync(0xffffffffu, top);
+          int E = static_cast<int>(top >> 7) - 127;
+          if (top == 0u) E = 14;
+          E = max(E, -100);
+          const float up = exp2i(14 - E) * sign, down = exp2i(E - 14);
+          uint32_t hv[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            hv[k] = pack_half2(__uint_as_float(wv[k] << 16) * up, __uint_as_float(wv[k] & 0xFFFF0000u) * up);
+          // lane: channels 16*lane .. +15: part lane / 4, chunks 2*(lane % 4), +1
+          uint8_t* dst = S.q[lane >> 2] + r * 128;
+          const int c0 = 2 * (lane & 3);
+          *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+          *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+          if (lane == 0) {
+            S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
+            S.row_lim[r] = pr < rows ? seen_by(a.q_pos[T.q0 + pr / a.heads], a.ratio, S.plan.ctx[T.b]) : 0;
+          }
         }
       }
       fence_proxy_async_smem();
@@ -339,26 +358,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const float inv = whole ? (l > 0.0f ? kRowScale / l : (l == 0.0f ? 0.0f : l)) : kRowScale;
       const long long orow = static_cast<long long>(T.q0) * a.heads + pr;
       float* part = partial_of(wsp, pair, off > 0 ? 0 : 1, 2 * kGRows);
+      if (whole) {
+        // Rows of bf16 into the space of Q and P (every product that read them
+        // is done), 16 bytes apart from a multiple of 128 so that the lanes'
+        // rows fall into different banks, then one bulk copy a row.
+        uint8_t* stage = S.q[0];
+#pragma unroll
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t r[32], h[16];
+          tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 b =
+                __floats2bfloat162_rn(__uint_as_float(r[2 * j]) * inv, __uint_as_float(r[2 * j + 1]) * inv);
+            h[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          const int ch = khalf * 256 + c;            // the upper lanes hold the other CTA's channels
+          uint4* dst = reinterpret_cast<uint4*>(stage + row * kStageRow + ch * 2);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(kBarSoft, kGSoftWarps * 32);
+        if (tid < kGRows && pr < rows) {
+          bulk_store_1d(out + orow * kKvDim, stage + row * kStageRow, kKvDim * 2);
+          bulk_store_wait_read();
+        }
+      } else {
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
-        tmem_ld_wait();
-        const int ch = khalf * 256 + c;              // the upper lanes hold the other CTA's channels
-        if (pr < rows) {
-          if (whole) {
-            uint32_t h[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 b =
-                  __floats2bfloat162_rn(__uint_as_float(r[2 * j]) * inv, __uint_as_float(r[2 * j + 1]) * inv);
-              h[j] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            uint4* dst = reinterpret_cast<uint4*>(out + orow * kKvDim + ch);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dst[j] = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(part + pr * kKvDim + ch);
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
+          tmem_ld_wait();
+          if (pr < rows) {
+            float4* dst = reinterpret_cast<float4*>(part + pr * kKvDim + khalf * 256 + c);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               dst[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
@@ -383,19 +417,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     }
   } else if (warp < kGSoftWarps + kGDeqWarps) {
     // ================= dequantisation =================
-    // Two warps fill two slots at a time, so that all groups' slots are under
-    // way at once: group q4 takes slots 2 q4 and 2 q4 + 1 of every half tile (8
-    // slots).  A granule is 32 channels of a key (16 code bytes).  A warp's load
-    // takes 8 keys x 64 bytes for K, 4 keys x 128 bytes for V (this CTA's
-    // channels are 256 neighbours): few cache lines an instruction, which the
-    // L1 looks up one by one.  A quarter warp holds 4 keys x 2 neighbouring
-    // granules: its 16-byte stores fall into eight different chunks.
-    const int dw = warp - kGSoftWarps, q4 = dw >> 1, wi = dw & 1;
-    // K: keys krow + 16 i, granule kg of slot 2 q4 + ksel
+    // Four warps fill two neighbouring slots (a pair) at a time; group grp
+    // takes pairs grp and grp + 2 of a half tile (8 slots).  A pair has to be
+    // filled within the time of the five slots before it: with two warps to a
+    // pair (all four pairs under way at once) that was the limit.  A granule is
+    // 32 channels of a key (16 code bytes).  A warp's load takes 8 keys x 64
+    // bytes for K, 4 keys x 128 bytes for V (this CTA's channels are 256
+    // neighbours): few cache lines an instruction, which the L1 looks up one by
+    // one.  A quarter warp holds 4 keys x 2 neighbouring granules: its 16-byte
+    // stores fall into eight different chunks.
+    const int dw = warp - kGSoftWarps, grp = dw >> 2, wi = dw & 3;
+    // K: keys krow + 32 i, granule kg of slot ksel of the pair
     const int krow = wi * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), kg = (lane >> 2) & 1, ksel = lane >> 4;
-    // V: keys vkey + 8 i of the two slots' 64, granule vg of this CTA's 8
+    // V: keys vkey + 16 i of the pair's 64, granule vg of this CTA's 8
     const int vkey = wi * 4 + (lane & 3), vg = (lane >> 3) * 2 + ((lane >> 2) & 1);
-    const int k_code = (2 * q4 + ksel) * 32 + kg * 16, k_sc = (2 * q4 + ksel) * 4 + kg * 2;
+    const int k_code = (2 * grp + ksel) * 32 + kg * 16, k_sc = (2 * grp + ksel) * 4 + kg * 2;
     const int v_code = static_cast<int>(rank) * 128 + vg * 16, v_sc = static_cast<int>(rank) * 16 + vg * 2;
     const uint32_t k_dst = krow * 128, v_dst = (vg >> 1) * 4096 + vkey * 128;
     const int k_c = kg * 4, v_c = (vg & 1) * 4;
@@ -410,80 +446,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       }
       return page * cache.page_size + key % cache.page_size;
     };
-    // Where a lane's 8 granules of a half tile lie: the first one's codes and
-    // scales, and the keys between two of them; no codes: zeros.
+    // Where a lane's 2 x 4 granules of a half tile lie: the codes and scales of
+    // each pair's first one, and the keys between two of a pair.  Keys that are
+    // not there read row 0 and a scale of 0 (mask): no branch lies between two
+    // granules, so their conversions overlap.
     struct Half {
-      const uint8_t *codes, *scales;
+      const uint8_t *codes[2], *scales[2];
+      uint32_t mask[2];
       int step;
     };
     auto half_k = [&](const DenseTile& T, int tile) {
       const int base = block_row(T, tile * kGKeys + static_cast<int>(rank) * 128);
-      const long long r = base + krow;
-      return Half{base < 0 ? nullptr : cache.kv_codes + r * kKvCodeBytes + k_code, cache.kv_scales + r * kKvScaleBytes + k_sc,
-                  16};
+      const long long r = max(base, 0) + krow;
+      const uint32_t mask = base < 0 ? 0u : 0x7F7Fu;
+      const uint8_t *c = cache.kv_codes + r * kKvCodeBytes + k_code, *x = cache.kv_scales + r * kKvScaleBytes + k_sc;
+      return Half{{c, c + 128}, {x, x + 16}, {mask, mask}, 32};
     };
     auto half_v = [&](const DenseTile& T, int tile) {
-      const int base = block_row(T, tile * kGKeys + (q4 >> 1) * 128);   // the slots' 64 keys lie in one block
-      const long long r = base + (q4 & 1) * 64 + vkey;
-      return Half{base < 0 ? nullptr : cache.kv_codes + r * kKvCodeBytes + v_code, cache.kv_scales + r * kKvScaleBytes + v_sc,
-                  8};
+      Half h;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {                  // a pair's 64 keys lie in one block of 128
+        const int base = block_row(T, tile * kGKeys + b * 128);
+        const long long r = max(base, 0) + grp * 64 + vkey;
+        h.codes[b] = cache.kv_codes + r * kKvCodeBytes + v_code;
+        h.scales[b] = cache.kv_scales + r * kKvScaleBytes + v_sc;
+        h.mask[b] = base < 0 ? 0u : 0x7F7Fu;
+      }
+      h.step = 16;
+      return h;
     };
     uint4 codes[8];                                  // the lane's granules of the half tile in turn
     uint32_t sc[8];
     auto load = [&](const Half& h, int i) {
-      codes[i] = make_uint4(0, 0, 0, 0);
-      sc[i] = 0;
-      if (h.codes != nullptr) {
-        codes[i] = *reinterpret_cast<const uint4*>(h.codes + i * h.step * kKvCodeBytes);
-        sc[i] = *reinterpret_cast<const uint16_t*>(h.scales + i * h.step * kKvScaleBytes);
-      }
+      codes[i] = *reinterpret_cast<const uint4*>(h.codes[i >> 2] + (i & 3) * h.step * kKvCodeBytes);
+      sc[i] = *reinterpret_cast<const uint16_t*>(h.scales[i >> 2] + (i & 3) * h.step * kKvScaleBytes) & h.mask[i >> 2];
     };
-    int n = 2 * q4;                                  // this group's next slot in the order of all slots
+    int n = 2 * grp;                                 // this group's next slot in the order of all slots
     bool ok = true;
     auto wait_empty = [&](int slot_no) {
-      if (ok && (S.abort_flag || !mbar_wait(&S.slot_empty[slot_no % kGSlots], ((slot_no / kGSlots) & 1) ^ 1, wait_ns)))
-        ok = false;
+      if (ok && !mbar_wait(&S.slot_empty[slot_no % kGSlots], ((slot_no / kGSlots) & 1) ^ 1, wait_ns)) ok = false;
       ok = __all_sync(0xffffffffu, ok) != 0;
     };
     auto arrive_full = [&](int slot_no) {
       if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.slot_full[slot_no % kGSlots]), 0));
     };
-    // granule i into a slot; its registers then receive that of the half tile after
-    auto put = [&](int i, uint8_t* dst, int chunk0, int x, const Half& next) {
-      uint4 o[4];
-      dequant_32(codes[i], sc[i], o);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((chunk0 + j) ^ x) << 4)) = o[j];
-      load(next, i);
-    };
-    auto store_k = [&](const Half& next) {           // both slots together: half a warp's lanes fill each
+    // Granules 4 p .. 4 p + 3 into a pair of slots; their registers then receive
+    // those of the next half tile.
+    auto store_pair = [&](int p, bool keys, const Half& next) {
       wait_empty(n);
       wait_empty(n + 1);
       if (ok) {
-        uint8_t* dst = S.slot[(n + ksel) % kGSlots] + k_dst;
+        uint8_t *d0, *d1;                            // of granules 4 p, 4 p + 1 and of 4 p + 2, 4 p + 3
+        if (keys) {
+          d0 = S.slot[(n + ksel) % kGSlots] + k_dst;
+          d1 = d0 + 64 * 128;
+        } else {
+          d0 = S.slot[n % kGSlots] + v_dst;
+          d1 = S.slot[(n + 1) % kGSlots] + v_dst;
+        }
+        const uint32_t step = keys ? 32 * 128 : 16 * 128;
+        const int c0 = keys ? k_c : v_c, x = keys ? krow & 7 : vkey & 7;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) put(i, dst + i * 16 * 128, k_c, krow & 7, next);
+        for (int i = 0; i < 4; ++i) {
+          uint4 o[4];
+          dequant_32(codes[4 * p + i], sc[4 * p + i], o);
+          uint8_t* dst = (i < 2 ? d0 : d1) + (i & 1) * step;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((c0 + j) ^ x) << 4)) = o[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load(next, 4 * p + i);
         fence_proxy_async_smem();
         __syncwarp();
         arrive_full(n);
         arrive_full(n + 1);
       }
-      n += 8;
+      n += 4;
     };
-    auto store_v = [&](const Half& next) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        wait_empty(n + b);
-        if (ok) {
-          uint8_t* dst = S.slot[(n + b) % kGSlots] + v_dst;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) put(b * 4 + i, dst + i * 8 * 128, v_c, vkey & 7, next);
-          fence_proxy_async_smem();
-          __syncwarp();
-          arrive_full(n + b);
-        }
-      }
-      n += 8;
+    auto store_half = [&](bool keys, const Half& next) {
+      store_pair(0, keys, next);
+      store_pair(1, keys, next);
     };
 
     long long pos = plan.lo;
@@ -500,10 +542,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
       for (int t = 0; ok && t < seg; ++t) {
-        store_k(t > 0 ? half_v(T, off + t - 1) : (seg > 1 ? half_k(T, off + 1) : half_v(T, off)));
-        if (t > 0) store_v(t + 1 < seg ? half_k(T, off + t + 1) : half_v(T, off + t));
+        store_half(true, t > 0 ? half_v(T, off + t - 1) : (seg > 1 ? half_k(T, off + 1) : half_v(T, off)));
+        if (t > 0) store_half(false, t + 1 < seg ? half_k(T, off + t + 1) : half_v(T, off + t));
       }
-      store_v(pos < plan.hi ? half_k(dense_tile(a, S.plan, ti + 1), 0) : Half{nullptr, nullptr, 0});
+      store_half(false, pos < plan.hi ? half_k(dense_tile(a, S.plan, ti + 1), 0) : half_v(T, off));   // (or nothing new)
     }
     if (!ok && lane == 0) {
       report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, static_cast<int>(rank), -n);
@@ -519,8 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     auto slot_ready = [&]() {
-      ok = S.abort_flag == 0 && mbar_wait_cluster_all(&S.slot_full[s], phase, wait_ns);
-      ok = __all_sync(0xffffffffu, ok) != 0;
+      ok = mbar_wait_cluster_all(&S.slot_full[s], phase, wait_ns);
       tc_fence_after();
     };
     auto next_slot = [&]() {

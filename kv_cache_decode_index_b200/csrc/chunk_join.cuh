@@ -11,7 +11,8 @@ constexpr int kMaxRanges = 296;                  // ranges of one launch: two CT
 constexpr int kWsRows = kMaxRanges * 2 * 64;     // rows of partial results: two tiles per range
 
 // The ranges' records, then two partial results per range (the tile that the
-// range starts inside, the tile that it ends inside): `rows` rows of 512 sums,
+// range starts inside, the tile that it ends inside): 512 sums of each of `rows`
+// rows, four channels of all rows together (the writers' lanes are rows), then
 // the rows' maxima (log2) and their sums.
 struct ChunkWorkspace {
   RangeRecord* rec;
@@ -28,12 +29,14 @@ __host__ __device__ inline float* partial_of(const ChunkWorkspace& w, int range,
   return w.part + (2 * static_cast<size_t>(range) + which) * (static_cast<size_t>(rows) * (kKvDim + 2));
 }
 
-template <int kThreads, int kStep>
-__device__ __forceinline__ void write_range_record(const DenseArgs& a, const DensePlanSmem<kThreads>& S,
-                                                   const DensePlan& plan, RangeRecord* rec) {
+// Where channel ch of a row lies in a partial result.
+__host__ __device__ inline int partial_at(int row, int ch, int rows) { return ((ch >> 2) * rows + row) * 4 + (ch & 3); }
+
+template <int kStep>
+__device__ __forceinline__ void write_range_record(const DenseArgs& a, const DensePlan& plan, RangeRecord* rec) {
   RangeRecord r = {plan.lo, plan.lo, plan.lo, 0, 0, plan.ctas, 0};
   if (plan.lo < plan.hi) {
-    const DenseTile t = dense_tile(a, S, plan.tile);
+    const DenseTile t = dense_tile(a, plan.start);
     r.tile_lo = plan.lo - plan.off;
     r.tile_hi = r.tile_lo + dense_steps<kStep>(t);
     r.q0 = t.q0;

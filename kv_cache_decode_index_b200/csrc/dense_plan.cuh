@@ -42,54 +42,63 @@ __device__ __forceinline__ int queries_of(const DenseArgs& a, int b, int kernel,
 // Entries that the query at token position p sees, of n_ctx.
 __device__ __forceinline__ int seen_by(int p, int ratio, int n_ctx) {
   if (p < 0) return 0;
-  const long long v = (static_cast<long long>(p) + 1) / ratio;
-  return v < n_ctx ? static_cast<int>(v) : n_ctx;
+  const uint32_t v = (static_cast<uint32_t>(p) + 1u) / static_cast<uint32_t>(ratio);
+  return v < static_cast<uint32_t>(n_ctx) ? static_cast<int>(v) : n_ctx;
 }
 
-// One query tile: request, first query, tokens, and the entries that any of
-// its queries sees.
+// One query tile: request, first query, tokens, the request's visible length,
+// and the entries that any of the tile's queries sees.
 struct DenseTile {
-  int b, q0, tokens, keys;
+  int b, q0, tokens, ctx, keys;
+};
+// A tile's place: request, and tile inside the request.
+struct TilePlace {
+  int b, j;
 };
 
 struct DensePlan {
-  int tiles;                             // of all requests
   int ctas;                              // CTAs that have work
-  long long steps;                       // W
   long long lo, hi;                      // this CTA's range
-  int tile;                              // where it starts: tile ...
+  TilePlace start;                       // where it starts: tile ...
   int off;                               // ... and step inside it
 };
 
-// Shared memory of the plan: tiles before each request, context lengths, and
-// the partial sums of the threads.
+// Shared memory of the plan (free again once dense_plan has returned and the
+// block has synchronised): tiles before each request, context lengths, and
+// the threads' partial sums.
 template <int kThreads>
 struct DensePlanSmem {
   int before[kMaxDenseBatch + 1];
   int ctx[kMaxDenseBatch];
   long long warp_sum[kThreads / 32];
-  long long total;
-  int tile, off;
+  TilePlace start;
+  int off;
 };
 
-template <int kThreads>
-__device__ __forceinline__ DenseTile dense_tile(const DenseArgs& a, const DensePlanSmem<kThreads>& S, int t) {
-  int lo = 0, hi = a.cache.batch;        // before[lo] <= t < before[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (S.before[mid] <= t) lo = mid;
-    else hi = mid;
-  }
+__device__ __forceinline__ DenseTile dense_tile(const DenseArgs& a, TilePlace p, int n, int ctx) {
   DenseTile d;
-  d.b = lo;
-  const int j = (t - S.before[lo]) * a.tile_tokens;
-  const int first = a.q_start ? a.q_start[lo] : lo, n = a.q_start ? a.q_start[lo + 1] - first : 1;
-  d.q0 = first + j;
+  d.b = p.b;
+  const int j = p.j * a.tile_tokens;
+  d.q0 = (a.q_start ? a.q_start[p.b] : p.b) + j;
   d.tokens = min(a.tile_tokens, n - j);
-  int keys = 0;
-  for (int i = 0; i < d.tokens; ++i) keys = max(keys, seen_by(a.q_pos[d.q0 + i], a.ratio, S.ctx[lo]));
-  d.keys = keys;
+  d.ctx = ctx;
+  int last = -1;                         // the largest position sees the most
+#pragma unroll 8
+  for (int i = 0; i < d.tokens; ++i) last = max(last, a.q_pos[d.q0 + i]);
+  d.keys = seen_by(last, a.ratio, ctx);
   return d;
+}
+__device__ __forceinline__ DenseTile dense_tile(const DenseArgs& a, TilePlace p) {
+  const long long capacity = static_cast<long long>(a.cache.max_pages_per_req) * a.cache.page_size;
+  return dense_tile(a, p, queries_of(a, p.b, 0, false), max(0, checked_ctx_len(a.cache, p.b, capacity, 0, false)));
+}
+// The place after p: the request's next tile, or the first of the next request
+// that has queries (there is one while a range is not done).
+__device__ __forceinline__ TilePlace next_tile(const DenseArgs& a, TilePlace p) {
+  if ((p.j + 1) * a.tile_tokens < queries_of(a, p.b, 0, false)) return TilePlace{p.b, p.j + 1};
+  int b = p.b + 1;
+  while (b < a.cache.batch && queries_of(a, b, 0, false) == 0) ++b;
+  return TilePlace{b, 0};
 }
 
 template <int kStep>
@@ -97,7 +106,7 @@ __device__ __forceinline__ int dense_steps(const DenseTile& t) {
   return max(1, (t.keys + kStep - 1) / kStep);   // a tile that sees nothing still writes its rows
 }
 
-// Every thread of the block calls this; S is filled and stays valid.
+// Every thread of the block calls this.
 template <int kThreads, int kStep>
 __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSmem<kThreads>& S, int cta, int ctas,
                                                 int kernel) {
@@ -126,12 +135,25 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
   }
   __syncthreads();
   DensePlan p;
-  p.tiles = S.before[a.cache.batch];
   // steps of a consecutive part of the tiles per thread
-  const int per = (p.tiles + kThreads - 1) / kThreads;
-  const int t0 = min(tid * per, p.tiles), t1 = min(t0 + per, p.tiles);
+  const int tiles = S.before[a.cache.batch];
+  const int per = (tiles + kThreads - 1) / kThreads;
+  const int t0 = min(tid * per, tiles), t1 = min(t0 + per, tiles);
+  auto place_of = [&](int t) {
+    int lo = 0, hi = a.cache.batch;      // before[lo] <= t < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (S.before[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    return TilePlace{lo, t - S.before[lo]};
+  };
+  auto steps_of = [&](TilePlace at) {
+    const int n = a.q_start ? a.q_start[at.b + 1] - a.q_start[at.b] : 1;
+    return dense_steps<kStep>(dense_tile(a, at, n, S.ctx[at.b]));
+  };
   long long mine = 0;
-  for (int t = t0; t < t1; ++t) mine += dense_steps<kStep>(dense_tile(a, S, t));
+  for (int t = t0; t < t1; ++t) mine += steps_of(place_of(t));
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -145,7 +167,6 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
     if (w < warp) before += S.warp_sum[w];
     total += S.warp_sum[w];
   }
-  p.steps = total;
   const long long most = (total + a.min_steps - 1) / a.min_steps;
   p.ctas = static_cast<int>(most < ctas ? most : ctas);
   if (cta < p.ctas) {
@@ -157,9 +178,10 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
   if (p.lo < p.hi && before <= p.lo && p.lo < before + mine) {
     long long at = before;
     for (int t = t0; t < t1; ++t) {
-      const int s = dense_steps<kStep>(dense_tile(a, S, t));
+      const TilePlace place = place_of(t);
+      const int s = steps_of(place);
       if (p.lo < at + s) {
-        S.tile = t;
+        S.start = place;
         S.off = static_cast<int>(p.lo - at);
         break;
       }
@@ -167,7 +189,7 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
     }
   }
   __syncthreads();
-  p.tile = S.tile;
+  p.start = S.start;
   p.off = S.off;
   return p;
 }

@@ -57,14 +57,15 @@ __global__ void __launch_bounds__(kCThreads, MR == 16 ? 2 : 1)
   const ChunkWorkspace wsp = split_chunk_ws(ws);
 
   const DensePlan plan = dense_plan<kCThreads, kChunk>(a, S.plan, blockIdx.x, gridDim.x, kKChunk);
-  if (tid == 0) write_range_record<kCThreads, kChunk>(a, S.plan, plan, &wsp.rec[blockIdx.x]);
+  if (tid == 0) write_range_record<kChunk>(a, plan, &wsp.rec[blockIdx.x]);
 
   const int r0 = lane >> 2;
   const int h0 = ht * 16 + r0, h1 = h0 + 8;
   long long pos = plan.lo;
   int off = plan.off;
-  for (int ti = plan.tile; pos < plan.hi; ++ti, off = 0) {
-    const DenseTile T = dense_tile(a, S.plan, ti);
+  TilePlace place = plan.start;
+  while (pos < plan.hi) {
+    const DenseTile T = dense_tile(a, place);
     const int steps = dense_steps<kChunk>(T);
     const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
     pos += seg;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kCThreads, MR == 16 ? 2 : 1)
       *reinterpret_cast<uint4*>(S.q + swz(r, 2 * lane + 1)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
       if (lane == 0) {
         S.qscale[r] = softmax_scale * down * kLog2e;
-        S.lim[r] = r < rows ? seen_by(a.q_pos[T.q0 + r / a.heads], a.ratio, S.plan.ctx[T.b]) : 0;
+        S.lim[r] = r < rows ? seen_by(a.q_pos[T.q0 + r / a.heads], a.ratio, T.ctx) : 0;
       }
     }
 
@@ -325,59 +326,67 @@ __global__ void __launch_bounds__(kCThreads, MR == 16 ? 2 : 1)
         for (int hf = 0; hf < 2; ++hf) {
           const int row = t * 16 + r0 + 8 * hf;
           if (row >= rows) continue;
-          float* dst = part + row * kKvDim + warp * kDimsPerWarp + 2 * (lane & 3);
 #pragma unroll
           for (int i = 0; i < kDimsPerWarp / 8; ++i)
-            *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o_acc[t][i][2 * hf], o_acc[t][i][2 * hf + 1]);
+            *reinterpret_cast<float2*>(part + partial_at(row, warp * kDimsPerWarp + 2 * (lane & 3) + i * 8, MR)) =
+                make_float2(o_acc[t][i][2 * hf], o_acc[t][i][2 * hf + 1]);
           if (warp == 0 && (lane & 3) == 0) {
             part[MR * kKvDim + row] = m_run[t][hf];
             part[MR * (kKvDim + 1) + row] = l_run[t][hf];
           }
         }
     }
+    if (pos < plan.hi) place = next_tile(a, place);
+    off = 0;
   }
 }
 
-// Joins the tiles that ranges cut: block (c, y) takes rows 4y .. 4y + 3 of the
-// tile that range c starts inside, if c is the first to do so; 128 threads
-// take four channels each of a row.
-constexpr int kJoinRows = 4;
+// Joins the tiles that ranges cut: block (c, x, y) takes 32 rows and 64
+// channels of the tile that range c starts inside, if c is the first to do so.
+// A lane is a row, a warp 8 channels.
+constexpr int kJoinRows = 32, kJoinChannels = 64;
 
-__global__ void __launch_bounds__(kJoinRows * kKvDim / 4)
+__global__ void __launch_bounds__(256)
     chunk_join_kernel(int heads, int tile_rows, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, void* ws) {
   const ChunkWorkspace wsp = split_chunk_ws(ws);
   const int c = blockIdx.x;
   const RangeRecord r = wsp.rec[c];
   if (c >= r.ctas || r.lo == r.tile_lo || wsp.rec[c - 1].lo > r.tile_lo) return;
-  const int row = blockIdx.y * kJoinRows + threadIdx.x / (kKvDim / 4), d = (threadIdx.x % (kKvDim / 4)) * 4;
+  const int row = blockIdx.z * kJoinRows + (threadIdx.x & 31);
+  const int ch = blockIdx.y * kJoinChannels + (threadIdx.x >> 5) * 8;
   if (row >= r.tokens * heads) return;
   int last = c;
   while (last + 1 < r.ctas && wsp.rec[last + 1].lo < r.tile_hi) ++last;
   // the tile's head came from range c - 1, which ended (or also began) with it
   float M = -INFINITY;
+#pragma unroll 4
   for (int k = c - 1; k <= last; ++k) M = fmaxf(M, partial_of(wsp, k, k < c ? 1 : 0, tile_rows)[tile_rows * kKvDim + row]);
   const float ref = M == -INFINITY ? 0.0f : M;
-  float l = 0.0f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.0f, o[8] = {};
 #pragma unroll 4
   for (int k = c - 1; k <= last; ++k) {
     const float* part = partial_of(wsp, k, k < c ? 1 : 0, tile_rows);
     const float f = exp2f(part[tile_rows * kKvDim + row] - ref);
     l = fmaf(part[tile_rows * (kKvDim + 1) + row], f, l);
-    const float4 v = *reinterpret_cast<const float4*>(part + row * kKvDim + d);
-    o.x = fmaf(v.x, f, o.x);
-    o.y = fmaf(v.y, f, o.y);
-    o.z = fmaf(v.z, f, o.z);
-    o.w = fmaf(v.w, f, o.w);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 v = *reinterpret_cast<const float4*>(part + partial_at(row, ch + 4 * h, tile_rows));
+      o[4 * h] = fmaf(v.x, f, o[4 * h]);
+      o[4 * h + 1] = fmaf(v.y, f, o[4 * h + 1]);
+      o[4 * h + 2] = fmaf(v.z, f, o[4 * h + 2]);
+      o[4 * h + 3] = fmaf(v.w, f, o[4 * h + 3]);
+    }
   }
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
   const long long orow = static_cast<long long>(r.q0) * heads + row;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  uint2 pk;
-  pk.x = *reinterpret_cast<const uint32_t*>(&lo);
-  pk.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(out + orow * kKvDim + d) = pk;
-  if (lse != nullptr && d == 0) lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
+  uint32_t pk[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * h] * inv, o[2 * h + 1] * inv);
+    pk[h] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(out + orow * kKvDim + ch) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  if (lse != nullptr && ch == 0) lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 template <int MR>
@@ -402,7 +411,7 @@ cudaError_t launch_chunk(const DenseArgs& a, const uint16_t* q, float scale, uin
 
 cudaError_t launch_chunk_join(int heads, int tile_rows, int ranges, uint16_t* out, float* lse, void* ws,
                               cudaStream_t stream) {
-  chunk_join_kernel<<<dim3(ranges, (tile_rows + kJoinRows - 1) / kJoinRows), kJoinRows * kKvDim / 4, 0, stream>>>(
+  chunk_join_kernel<<<dim3(ranges, kKvDim / kJoinChannels, (tile_rows + kJoinRows - 1) / kJoinRows), 256, 0, stream>>>(
       heads, tile_rows, reinterpret_cast<__nv_bfloat16*>(out), lse, ws);
   return cudaGetLastError();
 }

@@ -42,8 +42,9 @@ constexpr int kGSoftWarps = 4, kGDeqWarps = 8;
 constexpr int kGThreads = (kGSoftWarps + kGDeqWarps + 1) * 32;   // 416
 constexpr int kGKeys = 256;                  // keys of a tile
 constexpr int kGRows = 64;                   // query rows of one CTA
-constexpr int kGSlots = 7;
+constexpr int kGPairs = 4;                   // ring: pairs of slots
 constexpr int kSlotBytes = 16384;
+constexpr int kPairBytes = 2 * kSlotBytes;
 constexpr uint32_t kGTmemCols = 512;
 constexpr uint32_t kOCol = 0, kSCol = 256;   // O: 2 x 128 columns; S: 2 buffers of 128
 constexpr uint32_t kIdescS = idesc_f16_f32(128, 256, false, false);
@@ -57,12 +58,14 @@ constexpr float kRowScale = 256.0f;          // stored rows are 2^-8 of their va
 struct __align__(1024) PairSmem {
   uint8_t q[8][kGRows * 128];                // A of S: 64-channel parts
   uint8_t p[4][kGRows * 128];                // A of O: 64-key parts
-  uint8_t slot[kGSlots][kSlotBytes];
+  union {
+    uint8_t ring[kGPairs][kPairBytes];
+    DensePlanSmem<kGThreads> plan;           // before the first pair is filled
+  };
   float xchg[2][128];
   float row_scale[kGRows];
-  int row_lim[kGRows];
-  uint64_t slot_full[kGSlots];               // leader: both CTAs' dequantisation
-  uint64_t slot_empty[kGSlots];
+  uint64_t full[kGPairs];                    // leader: both CTAs' dequantisation
+  uint64_t empty[kGPairs];
   uint64_t s_full[2];
   uint64_t p_full;                           // leader: both CTAs' softmax
   uint64_t o_done;
@@ -70,7 +73,6 @@ struct __align__(1024) PairSmem {
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
-  DensePlanSmem<kGThreads> plan;
 };
 static_assert(sizeof(PairSmem::q) + sizeof(PairSmem::p) >= kGRows * kStageRow, "staged output rows");
 static_assert(offsetof(PairSmem, p) == sizeof(PairSmem::q), "P lies behind Q");
@@ -157,9 +159,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   const ChunkWorkspace wsp = split_chunk_ws(ws);
 
   if (tid == 0) {
-    for (int s = 0; s < kGSlots; ++s) {
-      mbar_init(&S.slot_full[s], 8);             // four warps of each CTA
-      mbar_init(&S.slot_empty[s], 1);
+    for (int s = 0; s < kGPairs; ++s) {
+      mbar_init(&S.full[s], 8);                  // four warps of each CTA
+      mbar_init(&S.empty[s], 1);
     }
     mbar_init(&S.s_full[0], 1);
     mbar_init(&S.s_full[1], 1);
@@ -177,7 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
   tc_fence_after();
   cluster_sync_all();
   const uint32_t tmem = S.tmem_base;
-  if (tid == 0 && rank == 0) write_range_record<kGThreads, kGKeys>(a, S.plan, plan, &wsp.rec[pair]);
+  if (tid == 0 && rank == 0) write_range_record<kGKeys>(a, plan, &wsp.rec[pair]);
 
   if (warp < kGSoftWarps) {
     // ================= softmax =================
@@ -189,12 +191,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     bool ok = true;
     long long pos = plan.lo;
     int off = plan.off;
-    for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0) {
-      const DenseTile T = dense_tile(a, S.plan, ti);
+    TilePlace place = plan.start;
+    while (ok && pos < plan.hi) {
+      const DenseTile T = dense_tile(a, place);
       const int steps = dense_steps<kGKeys>(T);
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
       const int rows = T.tokens * a.heads;           // of the pair
+      const int own = static_cast<int>(rank) * kGRows + row;
+      const int lim = own < rows ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : 0;
       // queries -> fp16 with a power-of-two scale per row (as bf16 they are
       // kept whole), eight rows' loads in flight
 #pragma unroll 1
@@ -213,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = r0 + i * kGSoftWarps, pr = static_cast<int>(rank) * kGRows + r;
+          const int r = r0 + i * kGSoftWarps;
           const uint32_t wv[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
           uint32_t top = 0;                          // exponent and mantissa of the largest magnitude (bf16 bits order like it)
 #pragma unroll
@@ -232,17 +237,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           const int c0 = 2 * (lane & 3);
           *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
           *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-          if (lane == 0) {
-            S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
-            S.row_lim[r] = pr < rows ? seen_by(a.q_pos[T.q0 + pr / a.heads], a.ratio, S.plan.ctx[T.b]) : 0;
-          }
+          if (lane == 0) S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
         }
       }
       fence_proxy_async_smem();
       named_bar_sync(kBarSoft, kGSoftWarps * 32);
       if (lane == 0) mbar_arrive_cluster(q_full);
       const float c2 = S.row_scale[row];
-      const int lim = S.row_lim[row];
       float m_ref = -INFINITY, l = 0.0f;
 
       for (int t = 0; t < seg; ++t, ++g) {
@@ -253,9 +254,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const bool masked = __any_sync(0xffffffffu, lim < key0 + 128);
+        const bool seen = __any_sync(0xffffffffu, lim > key0);       // by any row of this warp
         // tensor-memory loads run one part ahead of the arithmetic
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        {
+        if (seen) {
           uint32_t r[2][32];
           tmem_ld_32x32b_x32(s_addr, r[0]);
 #pragma unroll
@@ -288,7 +290,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         const bool careful = __any_sync(0xffffffffu, lim < key0 + 128 || !(fabsf(ref) < kFar));
         // the probabilities wait in registers (fp16) for the previous tile's P to be free
         uint32_t h[64];
-        {
+        if (!seen) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) h[j] = 0u;
+        } else {
           uint32_t r[2][16];
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           tmem_ld_32x32b_x16(s_addr, r[0]);
@@ -353,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       S.xchg[g & 1][tid] = l;
       named_bar_sync(kBarSoft, kGSoftWarps * 32);
       l = S.xchg[g & 1][row] + S.xchg[g & 1][row + 64];
-      const int pr = static_cast<int>(rank) * kGRows + row;
+      const int pr = own;
       const bool whole = seg == steps;
       const float inv = whole ? (l > 0.0f ? kRowScale / l : (l == 0.0f ? 0.0f : l)) : kRowScale;
       const long long orow = static_cast<long long>(T.q0) * a.heads + pr;
@@ -392,10 +397,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           tmem_ld_32x32b_x32(tmem + lane_base + kOCol + c, r);
           tmem_ld_wait();
           if (pr < rows) {
-            float4* dst = reinterpret_cast<float4*>(part + pr * kKvDim + khalf * 256 + c);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
+              *reinterpret_cast<float4*>(part + partial_at(pr, khalf * 256 + c + 4 * j, 2 * kGRows)) = make_float4(__uint_as_float(r[4 * j]) * inv, __uint_as_float(r[4 * j + 1]) * inv,
                                    __uint_as_float(r[4 * j + 2]) * inv, __uint_as_float(r[4 * j + 3]) * inv);
           }
         }
@@ -409,7 +413,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         }
       }
       tc_fence_before();
-      named_bar_sync(kBarSoft, kGSoftWarps * 32);    // Q, the row tables and O are free
+      named_bar_sync(kBarSoft, kGSoftWarps * 32);    // Q, the row table and O are free
+      if (pos < plan.hi) place = next_tile(a, place);
+      off = 0;
     }
     if (!ok) {
       if (lane == 0) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, static_cast<int>(rank), g);
@@ -481,28 +487,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       codes[i] = *reinterpret_cast<const uint4*>(h.codes[i >> 2] + (i & 3) * h.step * kKvCodeBytes);
       sc[i] = *reinterpret_cast<const uint16_t*>(h.scales[i >> 2] + (i & 3) * h.step * kKvScaleBytes) & h.mask[i >> 2];
     };
-    int n = 2 * grp;                                 // this group's next slot in the order of all slots
+    int n = grp;                                     // this group's next pair in the order of all pairs
     bool ok = true;
-    auto wait_empty = [&](int slot_no) {
-      if (ok && !mbar_wait(&S.slot_empty[slot_no % kGSlots], ((slot_no / kGSlots) & 1) ^ 1, wait_ns)) ok = false;
-      ok = __all_sync(0xffffffffu, ok) != 0;
-    };
-    auto arrive_full = [&](int slot_no) {
-      if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.slot_full[slot_no % kGSlots]), 0));
-    };
     // Granules 4 p .. 4 p + 3 into a pair of slots; their registers then receive
     // those of the next half tile.
     auto store_pair = [&](int p, bool keys, const Half& next) {
-      wait_empty(n);
-      wait_empty(n + 1);
+      const int x4 = n % kGPairs;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&S.empty[x4], ((n / kGPairs) & 1) ^ 1, wait_ns)) != 0;
+      n += 2;
       if (ok) {
         uint8_t *d0, *d1;                            // of granules 4 p, 4 p + 1 and of 4 p + 2, 4 p + 3
         if (keys) {
-          d0 = S.slot[(n + ksel) % kGSlots] + k_dst;
+          d0 = S.ring[x4] + ksel * kSlotBytes + k_dst;
           d1 = d0 + 64 * 128;
         } else {
-          d0 = S.slot[n % kGSlots] + v_dst;
-          d1 = S.slot[(n + 1) % kGSlots] + v_dst;
+          d0 = S.ring[x4] + v_dst;
+          d1 = d0 + kSlotBytes;
         }
         const uint32_t step = keys ? 32 * 128 : 16 * 128;
         const int c0 = keys ? k_c : v_c, x = keys ? krow & 7 : vkey & 7;
@@ -518,10 +518,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         for (int i = 0; i < 4; ++i) load(next, 4 * p + i);
         fence_proxy_async_smem();
         __syncwarp();
-        arrive_full(n);
-        arrive_full(n + 1);
+        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.full[x4]), 0));
       }
-      n += 4;
     };
     auto store_half = [&](bool keys, const Half& next) {
       store_pair(0, keys, next);
@@ -531,13 +529,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     long long pos = plan.lo;
     int off = plan.off;
     // the order of the MMAs: K(0), then K(t), V(t - 1), and V of the last tile
+    TilePlace place = plan.start;
+    DenseTile T = {};
     if (pos < plan.hi) {
-      const Half first = half_k(dense_tile(a, S.plan, plan.tile), off);
+      T = dense_tile(a, place);
+      const Half first = half_k(T, off);
 #pragma unroll
       for (int i = 0; i < 8; ++i) load(first, i);
     }
-    for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0) {
-      const DenseTile T = dense_tile(a, S.plan, ti);
+    while (ok && pos < plan.hi) {
       const int steps = dense_steps<kGKeys>(T);
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
@@ -545,7 +545,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         store_half(true, t > 0 ? half_v(T, off + t - 1) : (seg > 1 ? half_k(T, off + 1) : half_v(T, off)));
         if (t > 0) store_half(false, t + 1 < seg ? half_k(T, off + t + 1) : half_v(T, off + t));
       }
-      store_half(false, pos < plan.hi ? half_k(dense_tile(a, S.plan, ti + 1), 0) : half_v(T, off));   // (or nothing new)
+      const Half last = half_v(T, off + seg - 1);    // loaded again if nothing comes after it
+      off = 0;
+      if (pos < plan.hi) {
+        place = next_tile(a, place);
+        T = dense_tile(a, place);
+        store_half(false, half_k(T, 0));
+      } else {
+        store_half(false, last);
+      }
     }
     if (!ok && lane == 0) {
       report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, static_cast<int>(rank), -n);
@@ -555,65 +563,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     // ================= MMA issuer =================
     const bool issue = elect_one();
     const uint64_t q_desc = sw128_kmajor_desc(smem_u32(S.q[0])), p_desc = sw128_kmajor_desc(smem_u32(S.p[0]));
-    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.slot[0]));
-    const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(S.slot[0]), 4096);
-    int s = 0, g = 0, segs = 0;                      // slot in turn and its phase
+    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.ring[0]));
+    const uint64_t v_desc = sw128_mnmajor_desc(smem_u32(S.ring[0]), 4096);
+    int s = 0, g = 0, segs = 0;                      // pair of slots in turn and its phase
     uint32_t phase = 0;
     bool ok = true;
-    auto slot_ready = [&]() {
-      ok = mbar_wait_cluster_all(&S.slot_full[s], phase, wait_ns);
+    auto pair_ready = [&]() {
+      ok = mbar_wait_cluster_all(&S.full[s], phase, wait_ns);
       tc_fence_after();
+      return ok;
     };
-    auto next_slot = [&]() {
-      if (++s == kGSlots) {
+    auto next_pair = [&]() {
+      __syncwarp();
+      if (++s == kGPairs) {
         s = 0;
         phase ^= 1;
       }
     };
     auto scores = [&](int buf) {
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        slot_ready();
-        if (!ok) return;
+      for (int c = 0; c < 4; ++c) {
+        if (!pair_ready()) return;
         if (issue) {
-          const uint64_t ad = q_desc + c * (kGRows * 128 / 16), bd = k_desc + s * (kSlotBytes / 16);
+          const uint64_t ad = q_desc + c * (2 * kGRows * 128 / 16), bd = k_desc + s * (kPairBytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_pair(tmem + kSCol + buf * 128, ad + 2 * kk, bd + 2 * kk, kIdescS, (c | kk) > 0 ? 1u : 0u);
-          umma_commit_pair(&S.slot_empty[s]);
-          if (c == 7) umma_commit_pair(&S.s_full[buf]);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_pair(tmem + kSCol + buf * 128, ad + (kk >> 2) * (kGRows * 128 / 16) + (kk & 3) * 2,
+                          bd + (kk >> 2) * (kSlotBytes / 16) + (kk & 3) * 2, kIdescS, (c | kk) > 0 ? 1u : 0u);
+          umma_commit_pair(&S.empty[s]);
+          if (c == 3) umma_commit_pair(&S.s_full[buf]);
         }
-        __syncwarp();
-        next_slot();
+        next_pair();
       }
     };
     auto output = [&](int tile, bool first) {        // tile: running number
       ok = mbar_wait_cluster_all(&S.p_full, tile & 1, wait_ns);
       tc_fence_after();
 #pragma unroll 1
-      for (int j = 0; ok && j < 8; ++j) {
-        slot_ready();
-        if (!ok) return;
+      for (int j = 0; ok && j < 4; ++j) {
+        if (!pair_ready()) return;
         if (issue) {
-          const uint64_t ad = p_desc + (j >> 1) * (kGRows * 128 / 16) + (j & 1) * 4;
-          const uint64_t bd = v_desc + s * (kSlotBytes / 16);
+          const uint64_t ad = p_desc + j * (kGRows * 128 / 16), bd = v_desc + s * (kPairBytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
+          for (int kk = 0; kk < 4; ++kk)             // 16 of the pair's 64 keys
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              umma_f16_pair(tmem + kOCol + x * 128, ad + 2 * kk, bd + kk * (2048 / 16) + x * (8192 / 16), kIdescO,
+              umma_f16_pair(tmem + kOCol + x * 128, ad + 2 * kk,
+                            bd + (kk >> 1) * (kSlotBytes / 16) + (kk & 1) * (2048 / 16) + x * (8192 / 16), kIdescO,
                             first && (j | kk) == 0 ? 0u : 1u);
-          umma_commit_pair(&S.slot_empty[s]);
-          if (j == 7) umma_commit_pair(&S.o_done);
+          umma_commit_pair(&S.empty[s]);
+          if (j == 3) umma_commit_pair(&S.o_done);
         }
-        __syncwarp();
-        next_slot();
+        next_pair();
       }
     };
+    TilePlace place = plan.start;
     long long pos = plan.lo;
     int off = plan.off;
-    for (int ti = plan.tile; ok && pos < plan.hi; ++ti, off = 0, ++segs) {
-      const int steps = dense_steps<kGKeys>(dense_tile(a, S.plan, ti));
+    for (; ok && pos < plan.hi; ++segs, off = 0) {
+      const int steps = dense_steps<kGKeys>(dense_tile(a, place));
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
       ok = mbar_wait_cluster_all(&S.q_full, segs & 1, wait_ns);
@@ -623,6 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (ok && t > 0) output(g - 1, t == 1);
       }
       if (ok) output(g - 1, seg == 1);
+      if (pos < plan.hi) place = next_tile(a, place);
     }
     if (lane == 0 && !ok) {
       report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKChunk, -1, g);

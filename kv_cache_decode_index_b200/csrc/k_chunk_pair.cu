@@ -442,15 +442,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     const uint32_t k_dst = krow * 128, v_dst = (vg >> 1) * 4096 + vkey * 128;
     const int k_c = kg * 4, v_c = (vg & 1) * 4;
 
-    // first cache row of the 128 keys from `key` on, or -1: not seen by the tile, or a bad page
-    auto block_row = [&](const DenseTile& T, int key) {
-      if (key >= T.keys) return -1;
-      const int page = cache.page_table[static_cast<long long>(T.b) * cache.max_pages_per_req + key / cache.page_size];
-      if (page < 0 || page >= cache.num_pages) {
-        report_error(cache.err_word, CSA2_ERR_DEVICE_BOUNDS, kKChunk, T.b, key);
-        return -1;
+    // The pages of a tile's two blocks of 128 keys are looked up a tile ahead:
+    // fetch reads the table, resolve (half a tile later) turns the entries into
+    // first cache rows, or -1: not seen by the tile, or a bad page (recorded).
+    struct Blocks {
+      int page[2], off[2];
+    };
+    struct Rows {
+      int row[2];
+    };
+    auto fetch = [&](const DenseTile& T, int tile) {
+      Blocks x;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int key = tile * kGKeys + b * 128;
+        const int slot = key / cache.page_size;
+        x.page[b] = -2;
+        x.off[b] = key - slot * cache.page_size;
+        if (key < T.keys)
+          x.page[b] = cache.page_table[static_cast<long long>(T.b) * cache.max_pages_per_req + slot];
       }
-      return page * cache.page_size + key % cache.page_size;
+      return x;
+    };
+    auto resolve = [&](const DenseTile& T, int tile, const Blocks& x) {
+      Rows r;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const bool seen = tile * kGKeys + b * 128 < T.keys, good = x.page[b] >= 0 && x.page[b] < cache.num_pages;
+        if (seen && !good) report_error(cache.err_word, CSA2_ERR_DEVICE_BOUNDS, kKChunk, T.b, tile * kGKeys + b * 128);
+        r.row[b] = seen && good ? x.page[b] * cache.page_size + x.off[b] : -1;
+      }
+      return r;
     };
     // Where a lane's 2 x 4 granules of a half tile lie: the codes and scales of
     // each pair's first one, and the keys between two of a pair.  Keys that are
@@ -461,31 +483,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       uint32_t mask[2];
       int step;
     };
-    auto half_k = [&](const DenseTile& T, int tile) {
-      const int base = block_row(T, tile * kGKeys + static_cast<int>(rank) * 128);
+    auto half_k = [&](const Rows& rows) {
+      const int base = rank == 0 ? rows.row[0] : rows.row[1];
       const long long r = max(base, 0) + krow;
       const uint32_t mask = base < 0 ? 0u : 0x7F7Fu;
       const uint8_t *c = cache.kv_codes + r * kKvCodeBytes + k_code, *x = cache.kv_scales + r * kKvScaleBytes + k_sc;
       return Half{{c, c + 128}, {x, x + 16}, {mask, mask}, 32};
     };
-    auto half_v = [&](const DenseTile& T, int tile) {
+    auto half_v = [&](const Rows& rows) {
       Half h;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {                  // a pair's 64 keys lie in one block of 128
-        const int base = block_row(T, tile * kGKeys + b * 128);
-        const long long r = max(base, 0) + grp * 64 + vkey;
+        const long long r = max(rows.row[b], 0) + grp * 64 + vkey;
         h.codes[b] = cache.kv_codes + r * kKvCodeBytes + v_code;
         h.scales[b] = cache.kv_scales + r * kKvScaleBytes + v_sc;
-        h.mask[b] = base < 0 ? 0u : 0x7F7Fu;
+        h.mask[b] = rows.row[b] < 0 ? 0u : 0x7F7Fu;
       }
       h.step = 16;
       return h;
     };
     uint4 codes[8];                                  // the lane's granules of the half tile in turn
-    uint32_t sc[8];
+    uint32_t sc[8], mask[2];                         // (the mask is applied at use: here it would wait for the load)
     auto load = [&](const Half& h, int i) {
       codes[i] = *reinterpret_cast<const uint4*>(h.codes[i >> 2] + (i & 3) * h.step * kKvCodeBytes);
-      sc[i] = *reinterpret_cast<const uint16_t*>(h.scales[i >> 2] + (i & 3) * h.step * kKvScaleBytes) & h.mask[i >> 2];
+      sc[i] = *reinterpret_cast<const uint16_t*>(h.scales[i >> 2] + (i & 3) * h.step * kKvScaleBytes);
+      mask[i >> 2] = h.mask[i >> 2];
     };
     int n = grp;                                     // this group's next pair in the order of all pairs
     bool ok = true;
@@ -509,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint4 o[4];
-          dequant_32(codes[4 * p + i], sc[4 * p + i], o);
+          dequant_32(codes[4 * p + i], sc[4 * p + i] & mask[p], o);
           uint8_t* dst = (i < 2 ? d0 : d1) + (i & 1) * step;
 #pragma unroll
           for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(dst + (((c0 + j) ^ x) << 4)) = o[j];
@@ -531,9 +553,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     // the order of the MMAs: K(0), then K(t), V(t - 1), and V of the last tile
     TilePlace place = plan.start;
     DenseTile T = {};
+    Rows cur = {{-1, -1}};                           // of the tile whose K comes next
     if (pos < plan.hi) {
       T = dense_tile(a, place);
-      const Half first = half_k(T, off);
+      cur = resolve(T, off, fetch(T, off));
+      const Half first = half_k(cur);
 #pragma unroll
       for (int i = 0; i < 8; ++i) load(first, i);
     }
@@ -541,18 +565,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int steps = dense_steps<kGKeys>(T);
       const int seg = static_cast<int>(min(static_cast<long long>(steps - off), plan.hi - pos));
       pos += seg;
+      Rows prev = cur;
       for (int t = 0; ok && t < seg; ++t) {
-        store_half(true, t > 0 ? half_v(T, off + t - 1) : (seg > 1 ? half_k(T, off + 1) : half_v(T, off)));
-        if (t > 0) store_half(false, t + 1 < seg ? half_k(T, off + t + 1) : half_v(T, off + t));
+        const Blocks ahead = fetch(T, off + t + 1);  // (nothing is read behind the tile's keys)
+        if (t > 0) store_half(true, half_v(prev));
+        else store_half(true, seg > 1 ? half_k(resolve(T, off + 1, ahead)) : half_v(cur));
+        const Rows next = resolve(T, off + t + 1, ahead);
+        if (t > 0) store_half(false, t + 1 < seg ? half_k(next) : half_v(cur));
+        prev = cur;
+        cur = next;
       }
-      const Half last = half_v(T, off + seg - 1);    // loaded again if nothing comes after it
       off = 0;
       if (pos < plan.hi) {
         place = next_tile(a, place);
         T = dense_tile(a, place);
-        store_half(false, half_k(T, 0));
+        cur = resolve(T, 0, fetch(T, 0));
+        store_half(false, half_k(cur));
       } else {
-        store_half(false, last);
+        store_half(false, half_v(prev));             // (nothing comes after it: loaded once more)
       }
     }
     if (!ok && lane == 0) {

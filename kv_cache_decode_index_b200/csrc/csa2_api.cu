@@ -71,8 +71,8 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-csa2_status encode_rows_map(const void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
-                            CUtensorMap* map, int box_bytes = 0);
+csa2_status encode_rows_map(void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
+                            CUtensorMap* map);
 
 csa2_status encode_ik_map(const csa2_cache* c, int box_rows, CUtensorMap* map) {
   return encode_rows_map(c->ik_codes, static_cast<long long>(c->num_pages) * c->page_size, csa2::kIndexDim, box_rows,
@@ -80,9 +80,9 @@ csa2_status encode_ik_map(const csa2_cache* c, int box_rows, CUtensorMap* map) {
 }
 
 // 2-D map over `rows` rows of `row_bytes` bytes (uint8), box of box_rows
-// rows of box_bytes bytes (0: full rows).
-csa2_status encode_rows_map(const void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
-                            CUtensorMap* map, int box_bytes) {
+// full rows.
+csa2_status encode_rows_map(void* base, long long rows, int row_bytes, int box_rows, CUtensorMapSwizzle swizzle,
+                            CUtensorMap* map) {
   static EncodeFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -95,9 +95,9 @@ csa2_status encode_rows_map(const void* base, long long rows, int row_bytes, int
   if (fn == nullptr) return fail(CSA2_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available");
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes ? box_bytes : row_bytes), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(CSA2_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
@@ -675,11 +675,8 @@ csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, const int
                            "csa2_attn_mass_workspace_bytes"));
   DeviceInfo d;
   CSA2_TRY(device_info(&d));
-  CUtensorMap map;
-  CSA2_TRY(encode_rows_map(q, static_cast<long long>(n_queries) * H, csa2::kKvDim * 2, 32, CU_TENSOR_MAP_SWIZZLE_128B, &map,
-                           128));
-  const cudaError_t e = csa2::launch_attn_mass(*cache, n_queries, q_start, q_pos, ratio, H, scale, lse, mass, workspace,
-                                               map, d.sms, g_wait_limit_ns, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = csa2::launch_attn_mass(*cache, n_queries, q_start, q_pos, ratio, q, H, scale, lse, mass, workspace,
+                                               d.sms, g_wait_limit_ns, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "attn_mass launch");
 }
 

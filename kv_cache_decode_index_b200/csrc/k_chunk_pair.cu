@@ -28,10 +28,8 @@
 #include <cuda_bf16.h>
 #include <stddef.h>
 
-#include "attn_tile.cuh"
 #include "chunk_join.cuh"
-#include "cta_pair.cuh"
-#include "dense_plan.cuh"
+#include "pair_operands.cuh"
 #include "launch.h"
 
 namespace csa2 {
@@ -53,7 +51,6 @@ constexpr int kBarSoft = 1;
 constexpr float kRaise = 8.0f;               // log2 units a maximum may rise before O is rescaled
 constexpr int kStageRow = kKvDim * 2 + 16;     // bytes between staged output rows
 constexpr float kFar = 1048576.0f;           // 2^20: fp32 values are less than 1/8 apart below it
-constexpr float kRowScale = 256.0f;          // stored rows are 2^-8 of their value
 
 struct __align__(1024) PairSmem {
   uint8_t q[8][kGRows * 128];                // A of S: 64-channel parts
@@ -119,34 +116,6 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint3
   return d;
 }
 
-// 32 channels of a packed row (16 code bytes, two scale codes below 0x80 in the
-// low half of `sc`) -> four 16-byte chunks of fp16, each value times 2^-8.  Any
-// scale code gives finite values (rows that nobody sees may hold any bytes).
-__device__ __forceinline__ void dequant_32(uint4 codes, uint32_t sc, uint4 (&out)[4]) {
-  const uint32_t b0 = (sc & 0xFFu) << 7, b1 = (sc >> 8) << 7;
-  const uint32_t s0 = b0 | (b0 << 16), s1 = b1 | (b1 << 16);
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h[4];
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w[i]));
-    const uint32_t s = i < 2 ? s0 : s1;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), *reinterpret_cast<const __half2*>(&s));
-      h[k] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    out[i] = make_uint4(h[0], h[1], h[2], h[3]);
-  }
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     chunk_attn_pair_kernel(const DenseArgs a, const __nv_bfloat16* __restrict__ q, float scale,
                            __nv_bfloat16* __restrict__ out, float* __restrict__ lse, void* ws, uint64_t wait_ns) {
@@ -200,46 +169,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int rows = T.tokens * a.heads;           // of the pair
       const int own = static_cast<int>(rank) * kGRows + row;
       const int lim = own < rows ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : 0;
-      // queries -> fp16 with a power-of-two scale per row (as bf16 they are
-      // kept whole), eight rows' loads in flight
-#pragma unroll 1
-      for (int r0 = warp; r0 < kGRows; r0 += 8 * kGSoftWarps) {
-        uint4 v[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int pr = static_cast<int>(rank) * kGRows + r0 + i * kGSoftWarps;
-          v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-          if (pr < rows) {
-            const uint4* src =
-                reinterpret_cast<const uint4*>(q + (static_cast<long long>(T.q0) * a.heads + pr) * kKvDim) + lane * 2;
-            v[i][0] = src[0];
-            v[i][1] = src[1];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = r0 + i * kGSoftWarps;
-          const uint32_t wv[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
-          uint32_t top = 0;                          // exponent and mantissa of the largest magnitude (bf16 bits order like it)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) top = max(top, max(wv[k] & 0x7FFFu, (wv[k] >> 16) & 0x7FFFu));
-          top = __reduce_max_sync(0xffffffffu, top);
-          int E = static_cast<int>(top >> 7) - 127;
-          if (top == 0u) E = 14;
-          E = max(E, -100);
-          const float up = exp2i(14 - E) * sign, down = exp2i(E - 14);
-          uint32_t hv[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            hv[k] = pack_half2(__uint_as_float(wv[k] << 16) * up, __uint_as_float(wv[k] & 0xFFFF0000u) * up);
-          // lane: channels 16*lane .. +15: part lane / 4, chunks 2*(lane % 4), +1
-          uint8_t* dst = S.q[lane >> 2] + r * 128;
-          const int c0 = 2 * (lane & 3);
-          *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-          *reinterpret_cast<uint4*>(dst + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-          if (lane == 0) S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
-        }
-      }
+      load_query_rows<kGRows, kGSoftWarps>(q, static_cast<long long>(T.q0) * a.heads + static_cast<int>(rank) * kGRows,
+                                           rows - static_cast<int>(rank) * kGRows, kGRows, sign, S.q[0], warp, lane,
+                                           [&](int r, float down) {
+                                             S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
+                                           });
       fence_proxy_async_smem();
       named_bar_sync(kBarSoft, kGSoftWarps * 32);
       if (lane == 0) mbar_arrive_cluster(q_full);

@@ -2,73 +2,77 @@
 // call: mass[b][e] += sum over request b's queries and heads of
 // exp(scale q . v_e - lse), with the rows' log-sum-exp given.
 //
-// A matrix product with a sum over its columns: S^T = K Q^T on tcgen05 over a
-// pair of CTAs, M = 256 entries (128 per CTA), N = 256 query rows (128 loaded
-// by each CTA), bf16 operands (queries as they lie; the dequantised rows are
-// exact in bf16: at most 6 significant bits), fp32 sums.  Entries lie in the
-// lanes of tensor memory, so a thread sums its entry's weights over the
-// columns by itself.
-//   * the epilogue warps dequantise 128 entries per CTA into shared memory
-//     once per unit; the query rows stream past them;
-//   * warp 0: TMA of 64-channel parts of the query rows into a ring; warp 1 of
-//     the leader: the MMAs, into one of two 256-column accumulators; warps 2-9:
-//     two column halves x four lane quarters, exp2 and the sum.
-// Why a pair: one CTA alone would read 128 + 64 bytes of shared memory a cycle
-// (operands, and the arriving rows) where it has 128, and every SM would draw
-// 64 bytes a cycle from L2; the pair halves both.
-// The list of (256 entries, 256 rows) items is cut into equal ranges; cut
-// entries' sums are joined in a fixed order by a second launch.
+// A matrix product with a sum over its columns: S^T = V Q^T on tcgen05 over a
+// pair of CTAs, M = 256 entries (128 per CTA), N = up to 256 query rows (half
+// per CTA), K = 512.  Entries lie in the lanes of tensor memory, so a thread
+// sums its entry's weights over the columns by itself.
+//   * The query rows of a tile stay in shared memory (128 KB), fp16; the entries
+//     stream past them: eight warps dequantise 128 entries per CTA and tile
+//     into a ring of two 32 KB pairs of slots.  Entries are 288 bytes each where
+//     a query row is 1 KB, so this is the side to stream; for single tokens it
+//     is the only one that is long.
+//   * One warp of the leader issues the MMAs into two 256-column accumulators;
+//     four warps take exp2 and the sums.
+// Why a pair: shared memory gives 128 bytes a cycle.  One CTA alone would read
+// 128 (operands of M = N = 128) and write 64 (rows); the pair reads 64 and
+// writes 32 for each of its CTAs at the full MMA rate.
+//
+// The work is cut into equal ranges of (row tile, 256 entries) steps, ordered by
+// request, part of 4,096 entries, row tile, tile of entries: a pair holds a
+// part's sums in shared memory over all row tiles.  Parts that ranges cut are
+// joined in a fixed order by a second launch.
 #include <cuda_bf16.h>
 
-#include "attn_tile.cuh"
-#include "cta_pair.cuh"
-#include "dense_plan.cuh"
 #include "launch.h"
+#include "pair_operands.cuh"
 
 namespace csa2 {
 
 namespace {
 
-constexpr int kMKeys = 256;                       // entries per unit (both CTAs)
-constexpr int kMRows = 256;                       // query rows per item
-constexpr int kMStages = 5;
-constexpr int kMEpiWarps = 8;
-constexpr int kMThreads = 64 + kMEpiWarps * 32;   // 320
+constexpr int kMEpiWarps = 4, kMDeqWarps = 8;
+constexpr int kMThreads = (kMEpiWarps + kMDeqWarps + 1) * 32;   // 416
+constexpr int kMKeys = 256;                       // entries of a tile (both CTAs)
+constexpr int kMRows = 256;                       // query rows of a tile (both CTAs)
+constexpr int kMPart = 16;                        // tiles of entries whose sums a pair holds
+constexpr int kMRing = 2;
+constexpr int kMSlot = 128 * 128;                 // 128 rows x 64 channels
 constexpr int kMAcc = 2;
 constexpr uint32_t kMTmemCols = kMAcc * kMRows;   // 512
-constexpr int kAtomBytes = 128 * 128;             // 128 rows x 64 16-bit channels
-constexpr int kBoxRows = 32;                      // rows of one TMA box
 constexpr int kMaxPairs = 128;
 constexpr int kBarEpi = 1;
 
 struct __align__(1024) MassSmem {
-  uint8_t k[kKvDim / 64][kAtomBytes];             // A: this CTA's 128 entries
-  uint8_t q[kMStages][kAtomBytes];                // B: this CTA's half of the rows, 64 channels
-  float lse2[2][kMRows];                          // log2 of the rows' sums
-  int lim[2][kMRows];                             // entries seen by each row (0: no row)
-  float red[kMKeys / 2];
-  int before[kMaxDenseBatch + 1];                 // units before each request
-  long long at[kMaxDenseBatch + 1];               // items before each request
-  uint64_t full[kMStages];
-  uint64_t empty[kMStages];
+  uint8_t q[kKvDim / 64][kMSlot];                 // B: this CTA's half of the rows
+  uint8_t ring[kMRing][2 * kMSlot];               // A: 128 entries, 128 channels a pair
+  float col_scale[2][kMRows];                     // per column: factor of the scores (by turns: the
+                                                  // other CTA fills its half of the next one) ...
+  float col_lse2[kMRows];                         // ... log2 of the row's sum ...
+  int col_lim[kMRows];                            // ... and entries that it sees (0: no row)
+  float sum[kMPart * kMKeys / 2];                 // this CTA's entries of the part
+  int warp_min[kMEpiWarps];
+  int ctx[kMaxDenseBatch];
+  long long at[kMaxDenseBatch + 1];               // steps before each request
+  uint64_t full[kMRing];                          // leader: both CTAs' dequantisation
+  uint64_t empty[kMRing];
   uint64_t acc_full[kMAcc];
-  uint64_t acc_empty[kMAcc];
-  uint64_t k_full;
+  uint64_t acc_empty[kMAcc];                      // leader
+  uint64_t q_full;                                // leader
+  uint64_t scale_full;                            // the other CTA's rows' factors have arrived
   uint64_t drain;
   uint32_t tmem_base;
-  volatile int abort_flag;
 };
+static_assert(sizeof(MassSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
 // What a pair says of its range, for the joining launch.
 struct MassRecord {
-  long long lo, unit_lo, unit_hi;   // first item; first and past-the-last item of the unit it starts in
-  int b, k0;                        // that unit
+  long long lo, part_lo, part_hi;   // first step; first and past-the-last step of the part it starts in
+  int b, k0;                        // that part
   int pairs, pad;
 };
-
 struct MassWorkspace {
   MassRecord* rec;
-  float* part;    // [pairs][2][256]
+  float* part;    // [pairs][2][kMPart * kMKeys]
 };
 __host__ __device__ inline MassWorkspace split_mass_ws(void* ws) {
   MassWorkspace w;
@@ -77,19 +81,17 @@ __host__ __device__ inline MassWorkspace split_mass_ws(void* ws) {
   return w;
 }
 
-// Entry [k0 + 128 rank, + 128) of request b is there: visible length and page.
-__device__ __forceinline__ int page_row(const csa2_cache& c, int b, int key, bool report) {
-  const int page = c.page_table[static_cast<long long>(b) * c.max_pages_per_req + key / c.page_size];
-  if (page < 0 || page >= c.num_pages) {
-    if (report) report_error(c.err_word, CSA2_ERR_DEVICE_BOUNDS, kKMass, b, key);
-    return -1;
-  }
-  return page * c.page_size + key % c.page_size;
-}
+// A run of steps with one row tile: entries' tiles [kt0, kt1) of the part that
+// starts at tile `part` of request b.
+struct Run {
+  int b, ctx, q0, rows;             // rows: of the whole request
+  int part, rt, kt0, kt1;
+  long long part_lo, part_hi;       // steps of the whole part
+};
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
-    attn_mass_kernel(const DenseArgs a, const __grid_constant__ CUtensorMap q_map, float scale,
-                     const float* __restrict__ lse, float* __restrict__ mass, void* ws, uint64_t wait_ns) {
+    attn_mass_kernel(const DenseArgs a, const __nv_bfloat16* __restrict__ q, float scale, const float* __restrict__ lse,
+                     float* __restrict__ mass, void* ws, uint64_t wait_ns) {
   extern __shared__ uint8_t smem_raw[];
   MassSmem& S = *reinterpret_cast<MassSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -99,26 +101,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   const MassWorkspace wsp = split_mass_ws(ws);
   const long long capacity = static_cast<long long>(cache.max_pages_per_req) * cache.page_size;
 
-  // ---- plan: items of each request = (its units of 256 entries) x (its tiles of 256 rows) ----
+  // ---- plan: steps of each request = its tiles of entries x its row tiles ----
   for (int b = tid; b < cache.batch; b += kMThreads) {
     const int n = queries_of(a, b, kKMass, blockIdx.x == 0);
     const int ctx = n > 0 ? max(0, checked_ctx_len(cache, b, capacity, kKMass, blockIdx.x == 0)) : 0;
-    S.before[b + 1] = ctx;
+    S.ctx[b] = ctx;
     S.at[b + 1] = static_cast<long long>((ctx + kMKeys - 1) / kMKeys) *
                   ((static_cast<long long>(n) * a.heads + kMRows - 1) / kMRows);
   }
   if (tid == 0) {
-    for (int s = 0; s < kMStages; ++s) {
-      mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 1);
+    for (int i = 0; i < kMRing; ++i) {
+      mbar_init(&S.full[i], kMDeqWarps);         // four warps of each CTA
+      mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < kMAcc; ++i) {
       mbar_init(&S.acc_full[i], 1);
       mbar_init(&S.acc_empty[i], 2 * kMEpiWarps);
     }
-    mbar_init(&S.k_full, 2 * kMEpiWarps);
+    mbar_init(&S.q_full, 2 * kMEpiWarps);
+    mbar_init(&S.scale_full, kMEpiWarps);
     mbar_init(&S.drain, 1);
-    S.abort_flag = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -136,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       run += __shfl_sync(0xffffffffu, v, 31);
     }
     if (lane == 0) S.at[0] = 0;
-  } else if (warp == 1) {
+  } else if (warp == 12) {
     tmem_alloc_pair(&S.tmem_base, kMTmemCols);
   }
   tc_fence_before();
@@ -149,294 +151,355 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   const long long lo = pair < used ? total * pair / used : total;
   const long long hi = pair < used ? total * (pair + 1) / used : total;
 
-  // The range as units: request, entries, and the row tiles [t0, t1) of each.
-  struct Unit {
-    int b, ctx, k0, t0, t1, tiles, q0, rows;   // rows: of the whole request
-  };
-  auto unit_at = [&](long long pos, int b) {
-    Unit u;
+  // The run at step pos (b: a request not behind it).
+  auto run_at = [&](long long pos, int b) {
+    Run u;
     while (S.at[b + 1] <= pos) ++b;
     u.b = b;
-    u.ctx = S.before[b + 1];
+    u.ctx = S.ctx[b];
     u.q0 = a.q_start ? a.q_start[b] : b;
-    const int n = a.q_start ? a.q_start[b + 1] - u.q0 : 1;
-    u.rows = n * a.heads;
-    u.tiles = (u.rows + kMRows - 1) / kMRows;
-    const long long r = pos - S.at[b];
-    u.k0 = static_cast<int>(r / u.tiles) * kMKeys;
-    u.t0 = static_cast<int>(r % u.tiles);
-    u.t1 = static_cast<int>(min(static_cast<long long>(u.tiles), u.t0 + (hi - pos)));
+    u.rows = (a.q_start ? a.q_start[b + 1] - u.q0 : 1) * a.heads;
+    const int row_tiles = (u.rows + kMRows - 1) / kMRows, key_tiles = (u.ctx + kMKeys - 1) / kMKeys;
+    const long long r = pos - S.at[b], per = static_cast<long long>(kMPart) * row_tiles;
+    u.part = static_cast<int>(r / per) * kMPart;
+    const int tiles = min(kMPart, key_tiles - u.part);
+    const long long in = r % per;
+    u.rt = static_cast<int>(in / tiles);
+    u.kt0 = static_cast<int>(in % tiles);
+    u.kt1 = static_cast<int>(min(static_cast<long long>(tiles), u.kt0 + (hi - pos)));
+    u.part_lo = pos - in;
+    u.part_hi = u.part_lo + static_cast<long long>(tiles) * row_tiles;
     return u;
   };
-  // Whether any row of tile t sees entry k0 or later (every lane of a warp).
-  auto tile_seen = [&](const Unit& u, int t) {
-    const int first = (t * kMRows) / a.heads, n = min(kMRows, u.rows - t * kMRows) / a.heads;
-    int m = 0;
-    if (lane < n) m = seen_by(a.q_pos[u.q0 + first + lane], a.ratio, u.ctx);
-    return __any_sync(0xffffffffu, m > u.k0);
+  // Where the run's tiles end for this row tile: it sees nothing behind (every
+  // lane of a warp; at most 16 tokens).
+  auto seen_end = [&](const Run& u) {
+    const int first = (u.rt * kMRows) / a.heads, n = min(kMRows, u.rows - u.rt * kMRows) / a.heads;
+    int last = -1;
+    if (lane < n) last = a.q_pos[u.q0 + first + lane];
+    const int keys = seen_by(__reduce_max_sync(0xffffffffu, last), a.ratio, u.ctx);
+    return min(u.kt1, (keys + kMKeys - 1) / kMKeys - u.part);
   };
-  // N of the item: its rows, rounded up to 32.
-  auto columns = [&](const Unit& u, int t) { return (min(kMRows, u.rows - t * kMRows) + 31) & ~31; };
+  auto columns = [&](const Run& u) { return (min(kMRows, u.rows - u.rt * kMRows) + 31) & ~31; };
 
   if (tid == 0 && rank == 0) {
     MassRecord r = {lo, lo, lo, 0, 0, used, 0};
     if (lo < hi) {
-      const Unit u = unit_at(lo, 0);
-      r.unit_lo = lo - u.t0;
-      r.unit_hi = r.unit_lo + u.tiles;
+      const Run u = run_at(lo, 0);
+      r.part_lo = u.part_lo;
+      r.part_hi = u.part_hi;
       r.b = u.b;
-      r.k0 = u.k0;
+      r.k0 = u.part * kMKeys;
     }
     wsp.rec[pair] = r;
   }
 
-  if (warp == 0) {
-    // ================= producer =================
-    const uint64_t policy = l2_policy_evict_last();
-    int i = 0, b = 0;
-    bool ok = true;
+  bool ok = true;
+  if (warp < kMEpiWarps) {
+    // ================= query rows, exp2 and the sums =================
+    const uint32_t q_full = map_rank(smem_u32(&S.q_full), 0);
+    const uint32_t tm_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const float sign = scale < 0.0f ? -1.0f : 1.0f;
+    int item = 0, b = 0, held_b = -1, held_rt = -1, loads = 0, min_lim = 0;
+    bool fresh = true;                              // no part is held
     for (long long pos = lo; ok && pos < hi;) {
-      const Unit u = unit_at(pos, b);
+      const Run u = run_at(pos, b);
       b = u.b;
-      pos += u.t1 - u.t0;
-      for (int t = u.t0; ok && t < u.t1; ++t) {
-        if (!tile_seen(u, t)) continue;
-        const int N = columns(u, t), half = N / 2;      // a multiple of 16: boxes overrun into the other rows' place
-        const int boxes = (half + kBoxRows - 1) / kBoxRows;
-        const int row0 = u.q0 * a.heads + t * kMRows + static_cast<int>(rank) * half;
-        if (lane == 0) {
-          for (int c = 0; c < kKvDim / 64; ++c, ++i) {
-            const int s = i % kMStages;
-            if (S.abort_flag || !mbar_wait(&S.empty[s], ((i / kMStages) & 1) ^ 1, wait_ns)) {
-              ok = false;
-              break;
-            }
-            if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2 * boxes * kBoxRows * 128);
-            const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
-            for (int x = 0; x < boxes; ++x)
-              tma_load_2d_pair(S.q[s] + x * kBoxRows * 128, &q_map, bar, c * 128, row0 + x * kBoxRows, policy);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      pos += u.kt1 - u.kt0;
+      const int end = seen_end(u), N = columns(u), half = N / 2;
+      if (fresh) {
+        for (int i = tid; i < kMPart * kMKeys / 2; i += kMEpiWarps * 32) S.sum[i] = 0.0f;
+        fresh = false;
       }
-    }
-    if (lane == 0 && !ok) {
-      report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, static_cast<int>(rank), i);
-      S.abort_flag = 1;
-    }
-    // copies still in flight (counted on the leader's barriers)
-    if (lane == 0 && rank == 0 && !ok)
-      for (int j = i > kMStages ? i - kMStages : 0; j < i; ++j)
-        (void)mbar_wait(&S.full[j % kMStages], (j / kMStages) & 1, kWaitLimitNs / 2);
-  } else if (warp == 1 && rank == 0) {
-    // ================= MMA issuer =================
-    const bool issue = elect_one();
-    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.k[0])), q_desc = sw128_kmajor_desc(smem_u32(S.q[0]));
-    int s = 0, item = 0, units = 0, b = 0;      // units: those with an item that is computed
-    uint32_t phase = 0;
-    bool ok = true;
-    for (long long pos = lo; ok && pos < hi;) {
-      const Unit u = unit_at(pos, b);
-      b = u.b;
-      pos += u.t1 - u.t0;
-      bool loaded = false;
-      for (int t = u.t0; ok && t < u.t1; ++t) {
-        if (!tile_seen(u, t)) continue;
-        if (!loaded) {
-          ok = mbar_wait_cluster_all(&S.k_full, units & 1, wait_ns);
-          loaded = true;
-          ++units;
+      if (u.kt0 < end) {
+        // every product that read the held rows is done (their accumulators were awaited)
+        const bool load = u.b != held_b || u.rt != held_rt;
+        if (load) {
+          named_bar_sync(kBarEpi, kMEpiWarps * 32);     // the column tables are free
+          held_b = u.b;
+          held_rt = u.rt;
+          const int in_tile = min(kMRows, u.rows - u.rt * kMRows);
+          const long long row0 = static_cast<long long>(u.q0) * a.heads + u.rt * kMRows;
+          // this CTA's half of the rows; the column tables hold both halves
+          ++loads;
+          float* table = S.col_scale[loads & 1] + rank * half;
+          const uint32_t there = map_rank(smem_u32(table), rank ^ 1u);
+          load_query_rows<128, kMEpiWarps>(q, row0 + static_cast<int>(rank) * half, in_tile - static_cast<int>(rank) * half,
+                                           half, sign, S.q[0], warp, lane, [&](int r, float down) {
+                                             const float f = down * fabsf(scale) * kLog2e * kRowScale;
+                                             table[r] = f;
+                                             st_cluster(there + r * 4, f);
+                                           });
+          if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(&S.scale_full), rank ^ 1u));
+          int lowest = 0x7FFFFFFF;
+          for (int c = tid; c < N; c += kMEpiWarps * 32) {
+            int lim = 0;
+            float l2 = 0.0f;
+            if (c < in_tile) {
+              lim = seen_by(a.q_pos[u.q0 + (u.rt * kMRows + c) / a.heads], a.ratio, u.ctx);
+              l2 = lse[row0 + c] * kLog2e;
+            }
+            S.col_lim[c] = lim;
+            S.col_lse2[c] = l2;
+            lowest = min(lowest, lim);
+          }
+          min_lim = __reduce_min_sync(0xffffffffu, lowest);
+          if (lane == 0) S.warp_min[warp] = min_lim;
+          fence_proxy_async_smem();
+          named_bar_sync(kBarEpi, kMEpiWarps * 32);
+          min_lim = min(min(S.warp_min[0], S.warp_min[1]), min(S.warp_min[2], S.warp_min[3]));
+          if (lane == 0) mbar_arrive_cluster(q_full);
+          ok = mbar_wait_cluster_all(&S.scale_full, (loads - 1) & 1, wait_ns);
         }
-        const uint32_t idesc = idesc_f16_f32(kMKeys, columns(u, t), true, false);
+      }
+      for (int kt = u.kt0; ok && kt < end; ++kt, ++item) {
+        const int k0 = (u.part + kt) * kMKeys, key0 = k0 + static_cast<int>(rank) * (kMKeys / 2);
+        const int key = key0 + tid;
+        int page = -1;                               // of this CTA's entries
+        if (key0 < u.ctx) page = cache.page_table[static_cast<long long>(u.b) * cache.max_pages_per_req + key0 / cache.page_size];
+        const bool mask = min_lim < min(k0 + kMKeys, u.ctx);
         const int acc = item % kMAcc;
-        ok = mbar_wait_cluster_all(&S.acc_empty[acc], ((item / kMAcc) & 1) ^ 1, wait_ns) && ok;
+        ok = mbar_wait_warp(&S.acc_full[acc], (item / kMAcc) & 1, wait_ns);
+        ok = !named_bar_or(kBarEpi, kMEpiWarps * 32, !ok);
+        if (!ok) break;
         tc_fence_after();
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t r[2][32];
+        tmem_ld_32x32b_x32(tm_lane + acc * kMRows, r[0]);
 #pragma unroll 1
-        for (int c = 0; ok && c < kKvDim / 64; ++c) {
-          ok = __all_sync(0xffffffffu, S.abort_flag == 0 && mbar_wait(&S.full[s], phase, wait_ns)) != 0;
-          if (!ok) break;
-          tc_fence_after();
-          if (issue) {
-            const uint64_t ad = k_desc + c * (kAtomBytes / 16), bd = q_desc + s * (kAtomBytes / 16);
+        for (int c = 0; c < N; c += 64) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_pair(tmem + acc * kMRows, ad + 2 * kk, bd + 2 * kk, idesc, (c | kk) > 0 ? 1u : 0u);
-            umma_commit_pair(&S.empty[s]);
-            if (c == kKvDim / 64 - 1) umma_commit_pair(&S.acc_full[acc]);
-          }
-          __syncwarp();
-          if (++s == kMStages) {
-            s = 0;
-            phase ^= 1;
-          }
-        }
-        ++item;
-      }
-    }
-    if (lane == 0 && !ok) {
-      report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, -1, item);
-      S.abort_flag = 1;
-    }
-    __syncwarp();
-    if (issue) umma_commit_pair(&S.drain);
-    (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
-  } else if (warp == 1) {
-    if (lane == 0) (void)mbar_wait(&S.drain, 0, 2 * kWaitLimitNs);   // the leader's last arrival here
-  } else {
-    // ================= dequantisation and epilogue =================
-    const int et = tid - 64;                       // 0..255
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const float c2 = scale * kLog2e;
-    const uint32_t k_full = map_rank(smem_u32(&S.k_full), 0);
-    // The unit's 128 entries of this CTA, dequantised to bf16.  16-byte
-    // granules (32 channels): a warp takes 8 rows x 4 granules, so that the
-    // 16-byte stores of a quarter warp fall into different banks.
-    auto load_keys = [&](int base) {
-      for (int it = 0; it < 8; ++it) {
-        const int x = it * kMEpiWarps + (warp - 2);             // 64 groups of (8 rows, 4 granules)
-        const int row = (x >> 2) * 8 + (lane & 7), g = (x & 3) * 4 + (lane >> 3);
-        uint4 hv[4] = {};
-        if (base >= 0) {
-          const long long r = base + row;
-          const uint4 cv = *reinterpret_cast<const uint4*>(cache.kv_codes + r * kKvCodeBytes + g * 16);
-          const uint32_t sc = *reinterpret_cast<const uint16_t*>(cache.kv_scales + r * kKvScaleBytes + g * 2);
-          dequant16(cv, sc, hv);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&hv[j]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-              const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);   // exact: 6 significant bits
-              w[k] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int chunk = (g & 1) * 4 + j;
-          *reinterpret_cast<uint4*>(S.k[g >> 1] + row * 128 + ((chunk ^ (row & 7)) << 4)) = hv[j];
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(k_full);
-    };
-    int item = 0, b = 0;
-    bool ok = true;
-    for (long long pos = lo; ok && pos < hi;) {
-      const Unit u = unit_at(pos, b);
-      b = u.b;
-      pos += u.t1 - u.t0;
-      bool loaded = false;
-      const int key0 = u.k0 + static_cast<int>(rank) * (kMKeys / 2);
-      const int base = key0 < u.ctx ? page_row(cache, u.b, key0, et == 0) : -1;
-      const int key = key0 + quarter * 32 + lane;
-      float sum = 0.0f;
-      for (int t = u.t0; t < u.t1; ++t) {
-        // this item's rows: a column per epilogue thread
-        const int buf = item & 1;
-        const int in_tile = min(kMRows, u.rows - t * kMRows);
-        const int first = (t * kMRows) / a.heads, N = columns(u, t);
-        int lim = 0;
-        float l2 = 0.0f;
-        if (et < in_tile) {
-          lim = seen_by(a.q_pos[u.q0 + first + et / a.heads], a.ratio, u.ctx);
-          l2 = lse[static_cast<long long>(u.q0) * a.heads + t * kMRows + et] * kLog2e;
-        }
-        const bool any = named_bar_or(kBarEpi, kMEpiWarps * 32, lim > u.k0);
-        if (!any) continue;
-        if (!loaded) {
-          load_keys(base);
-          loaded = true;
-        }
-        S.lse2[buf][et] = l2;
-        S.lim[buf][et] = lim;
-        const bool mask = named_bar_or(kBarEpi, kMEpiWarps * 32, et < N && lim < min(u.k0 + kMKeys, u.ctx));
-        const int acc = item % kMAcc;
-        ok = ok && mbar_wait_warp_backoff(&S.acc_full[acc], (item / kMAcc) & 1, wait_ns);
-        ++item;
-        if (!named_bar_or(kBarEpi, kMEpiWarps * 32, !ok)) {
-          tc_fence_after();
-          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          for (int c = half * (kMRows / 2); c < min((half + 1) * (kMRows / 2), N); c += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(tmem + acc * kMRows + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
+          for (int h = 0; h < 2; ++h) {
+            const int c1 = c + h * 32;
+            if (c1 >= N) break;
             tmem_ld_wait();
+            if (c1 + 32 < N) tmem_ld_32x32b_x32(tm_lane + acc * kMRows + c1 + 32, r[h ^ 1]);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(&S.lse2[buf][c + j]);
-              const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
+              const float4 s4 = *reinterpret_cast<const float4*>(&S.col_scale[loads & 1][c1 + j]);
+              const float4 l4 = *reinterpret_cast<const float4*>(&S.col_lse2[c1 + j]);
+              const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
               if (mask) {
-                const int4 m4 = *reinterpret_cast<const int4*>(&S.lim[buf][c + j]);
+                const int4 m4 = *reinterpret_cast<const int4*>(&S.col_lim[c1 + j]);
                 const int mv[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float p = ex2(fmaf(__uint_as_float(r[j + k]), c2, -lv[k]));
+                  const float p = ex2(fmaf(__uint_as_float(r[h][j + k]), sv[k], -lv[k]));
                   part[k] += key < mv[k] ? p : 0.0f;
                 }
               } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) part[k] += ex2(fmaf(__uint_as_float(r[j + k]), c2, -lv[k]));
+                for (int k = 0; k < 4; ++k) part[k] += ex2(fmaf(__uint_as_float(r[h][j + k]), sv[k], -lv[k]));
               }
             }
           }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
-          tc_fence_before();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acc_empty[acc]), 0));
+        if (page >= 0 && page < cache.num_pages) S.sum[kt * (kMKeys / 2) + tid] += (part[0] + part[1]) + (part[2] + part[3]);
+      }
+      // the part's end, or the range's: the entries' weights, or this pair's share of them
+      if (ok && (pos >= hi || pos >= u.part_hi)) {
+        const bool whole = u.part_lo >= lo && u.part_hi <= hi;
+        float* share = wsp.part + (2 * static_cast<size_t>(pair) + (u.part_lo < lo ? 0 : 1)) * (kMPart * kMKeys);
+#pragma unroll 4
+        for (int kt = 0; kt < kMPart; ++kt) {
+          const int in = kt * kMKeys + static_cast<int>(rank) * (kMKeys / 2) + tid, key = u.part * kMKeys + in;
+          const float s = S.sum[kt * (kMKeys / 2) + tid];
+          if (!whole) share[in] = s;
+          else if (key < u.ctx && s != 0.0f) mass[u.b * capacity + key] += s;
+        }
+        fresh = true;
+      }
+    }
+    if (!ok && lane == 0) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, static_cast<int>(rank), item);
+  } else if (warp < kMEpiWarps + kMDeqWarps) {
+    // ================= dequantisation =================
+    // Four warps fill a pair of slots; group grp takes pairs grp and grp + 2 of a
+    // tile's four.  A granule is 32 channels of an entry; lane: keys krow + 32 i,
+    // granule kg of slot ksel.  A quarter warp holds 4 entries x 2 neighbouring
+    // granules: its 16-byte stores fall into eight different chunks.
+    const int dw = warp - kMEpiWarps, grp = dw >> 2, wi = dw & 3;
+    const int krow = wi * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), kg = (lane >> 2) & 1, ksel = lane >> 4;
+    const int k_code = (2 * grp + ksel) * 32 + kg * 16, k_sc = (2 * grp + ksel) * 4 + kg * 2;
+    uint4 codes[8];                                  // the lane's granules of the tile in turn
+    uint32_t sc[8], mask = 0;
+    // The page of this CTA's 128 entries is looked up a tile ahead (fetch);
+    // row_of_page, half a tile later, gives their first cache row, or -1: not
+    // there, or a bad page (recorded).
+    struct Place {
+      int b, key, page, off;
+    };
+    auto fetch = [&](const Run& u, int kt) {
+      Place x;
+      x.b = u.b;
+      x.key = (u.part + kt) * kMKeys + static_cast<int>(rank) * (kMKeys / 2);
+      const int slot = x.key / cache.page_size;
+      x.off = x.key - slot * cache.page_size;
+      x.page = -2;
+      if (x.key < u.ctx) x.page = cache.page_table[static_cast<long long>(u.b) * cache.max_pages_per_req + slot];
+      return x;
+    };
+    auto row_of_page = [&](const Place& x) {
+      if (x.page >= 0 && x.page < cache.num_pages) return x.page * cache.page_size + x.off;
+      if (x.page != -2) report_error(cache.err_word, CSA2_ERR_DEVICE_BOUNDS, kKMass, x.b, x.key);
+      return -1;
+    };
+    const uint8_t *cp = cache.kv_codes, *sp = cache.kv_scales;   // of the tile to be loaded
+    uint32_t next_mask = 0;
+    auto aim = [&](int base) {
+      const long long r = max(base, 0) + krow;       // entries that are not there read row 0 with a scale of 0
+      cp = cache.kv_codes + r * kKvCodeBytes + k_code;
+      sp = cache.kv_scales + r * kKvScaleBytes + k_sc;
+      next_mask = base < 0 ? 0u : 0x7F7Fu;
+    };
+    auto load = [&](int i) {
+      codes[i] = *reinterpret_cast<const uint4*>(cp + (i >> 2) * 128 + (i & 3) * 32 * kKvCodeBytes);
+      sc[i] = *reinterpret_cast<const uint16_t*>(sp + (i >> 2) * 16 + (i & 3) * 32 * kKvScaleBytes);
+    };
+    // The tiles in order: run by run, the visible ones.
+    int b = 0;
+    long long pos = lo;
+    Run u = {};
+    int kt = 0, end = 0;
+    auto next_tile_of = [&]() {                      // advances to a tile; false at the range's end
+      ++kt;
+      while (kt >= end) {
+        if (pos >= hi) return false;
+        u = run_at(pos, b);
+        b = u.b;
+        pos += u.kt1 - u.kt0;
+        kt = u.kt0;
+        end = seen_end(u);
+      }
+      return true;
+    };
+    bool have = next_tile_of(), more = false;        // a tile is loaded; another one comes after it
+    Place ahead = {};
+    if (have) {
+      aim(row_of_page(fetch(u, kt)));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load(i);
+      mask = next_mask;
+      more = next_tile_of();
+      if (more) ahead = fetch(u, kt);
+    }
+    int n = grp;                                     // this group's next pair in the order of all pairs
+    while (ok && have) {
+      have = more;
+      if (more) {
+        aim(row_of_page(ahead));
+        more = next_tile_of();
+        if (more) ahead = fetch(u, kt);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p, n += 2) {
+        const int x2 = n % kMRing;
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&S.empty[x2], ((n / kMRing) & 1) ^ 1, wait_ns)) != 0;
+        if (!ok) continue;
+        uint8_t* dst = S.ring[x2] + ksel * kMSlot + krow * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 o[4];
+          dequant_32(codes[4 * p + i], sc[4 * p + i] & mask, o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + i * 32 * 128 + (((kg * 4 + j) ^ (krow & 7)) << 4)) = o[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load(4 * p + i); // the next tile's (at the end: the last one's again)
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.full[x2]), 0));
+      }
+      mask = next_mask;
+    }
+    if (!ok && lane == 0) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, static_cast<int>(rank), -n);
+  } else if (rank == 0) {
+    // ================= MMA issuer =================
+    const bool issue = elect_one();
+    const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.ring[0])), q_desc = sw128_kmajor_desc(smem_u32(S.q[0]));
+    int s = 0, item = 0, loads = 0, b = 0, held_b = -1, held_rt = -1;
+    uint32_t phase = 0;
+    for (long long pos = lo; ok && pos < hi;) {
+      const Run u = run_at(pos, b);
+      b = u.b;
+      pos += u.kt1 - u.kt0;
+      const int end = seen_end(u);
+      if (u.kt0 >= end) continue;
+      if (u.b != held_b || u.rt != held_rt) {
+        held_b = u.b;
+        held_rt = u.rt;
+        ok = mbar_wait_cluster_all(&S.q_full, loads & 1, wait_ns);
+        ++loads;
+      }
+      const uint32_t idesc = idesc_f16_f32(kMKeys, columns(u), false, false);
+      for (int kt = u.kt0; ok && kt < end; ++kt, ++item) {
+        const int acc = item % kMAcc;
+        ok = mbar_wait_cluster_all(&S.acc_empty[acc], ((item / kMAcc) & 1) ^ 1, wait_ns);
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; ok && c < 4; ++c) {
+          ok = mbar_wait_cluster_all(&S.full[s], phase, wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          if (issue) {
+            const uint64_t ad = k_desc + s * (2 * kMSlot / 16), bd = q_desc + c * (2 * kMSlot / 16);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_f16_pair(tmem + acc * kMRows, ad + (kk >> 2) * (kMSlot / 16) + (kk & 3) * 2,
+                            bd + (kk >> 2) * (kMSlot / 16) + (kk & 3) * 2, idesc, (c | kk) > 0 ? 1u : 0u);
+            umma_commit_pair(&S.empty[s]);
+            if (c == 3) umma_commit_pair(&S.acc_full[acc]);
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acc_empty[acc]), 0));
-        } else {
-          ok = false;
-          break;
+          if (++s == kMRing) {
+            s = 0;
+            phase ^= 1;
+          }
         }
       }
-      // both column halves, then the entry's weight or the pair's part of it
-      if (half == 1) S.red[quarter * 32 + lane] = sum;
-      named_bar_sync(kBarEpi, kMEpiWarps * 32);
-      if (half == 0 && ok) {
-        sum += S.red[quarter * 32 + lane];
-        if (u.t1 - u.t0 == u.tiles) {
-          if (key < u.ctx && base >= 0) mass[u.b * capacity + key] += sum;
-        } else {
-          wsp.part[(2 * pair + (u.t0 > 0 ? 0 : 1)) * kMKeys + static_cast<int>(rank) * (kMKeys / 2) + quarter * 32 +
-                   lane] = base >= 0 ? sum : 0.0f;
-        }
-      }
-      named_bar_sync(kBarEpi, kMEpiWarps * 32);
     }
-    if (!ok && lane == 0) {
-      report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, static_cast<int>(rank), -item);
-      S.abort_flag = 1;
-    }
+    if (lane == 0 && !ok) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, -1, item);
+    __syncwarp();
+    if (issue) umma_commit_pair(&S.drain);
+    (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
+  } else {
+    if (lane == 0) (void)mbar_wait(&S.drain, 0, 4 * kWaitLimitNs);   // the leader's last arrival here
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();          // every MMA has completed, no barrier of the other CTA is touched after this
-  if (warp == 1) tmem_release_pair(tmem, kMTmemCols);
+  if (warp == 12) tmem_release_pair(tmem, kMTmemCols);
 }
 
-// Joins the units that ranges cut: block c takes the unit that pair c starts
-// inside, if c is the first to do so.
+// Joins the parts that ranges cut: block (c, y) takes 256 entries of the part
+// that pair c starts inside, if c is the first to do so.
 __global__ void __launch_bounds__(kMKeys) attn_mass_join_kernel(const csa2_cache cache, float* __restrict__ mass, void* ws) {
   const MassWorkspace wsp = split_mass_ws(ws);
   const int c = blockIdx.x;
   const MassRecord r = wsp.rec[c];
-  if (c >= r.pairs || r.lo == r.unit_lo || wsp.rec[c - 1].lo > r.unit_lo) return;
-  float sum = wsp.part[(2 * (c - 1) + 1) * kMKeys + threadIdx.x];
-  for (int k = c; k < r.pairs && wsp.rec[k].lo < r.unit_hi; ++k) sum += wsp.part[2 * k * kMKeys + threadIdx.x];
+  if (c >= r.pairs || r.lo == r.part_lo || wsp.rec[c - 1].lo > r.part_lo) return;
+  const int in = blockIdx.y * kMKeys + threadIdx.x, key = r.k0 + in;
+  if (key >= cache.ctx_len[r.b]) return;
+  constexpr size_t kShare = kMPart * kMKeys;
+  float sum = wsp.part[(2 * static_cast<size_t>(c - 1) + 1) * kShare + in];
+  for (int k = c; k < r.pairs && wsp.rec[k].lo < r.part_hi; ++k) sum += wsp.part[2 * static_cast<size_t>(k) * kShare + in];
   const long long capacity = static_cast<long long>(cache.max_pages_per_req) * cache.page_size;
-  const int key = r.k0 + threadIdx.x, ctx = cache.ctx_len[r.b];
-  if (key < ctx) mass[r.b * capacity + key] += sum;
+  if (sum != 0.0f) mass[r.b * capacity + key] += sum;
 }
 
 }  // namespace
 
-size_t attn_mass_workspace_bytes() { return kMaxPairs * (sizeof(MassRecord) + 2 * kMKeys * sizeof(float)); }
+size_t attn_mass_workspace_bytes() {
+  return kMaxPairs * (sizeof(MassRecord) + 2 * static_cast<size_t>(kMPart) * kMKeys * sizeof(float));
+}
 
 cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
-                             int ratio, int H, float scale, const float* lse, float* mass, void* ws,
-                             const CUtensorMap& q_map, int num_sms, uint64_t wait_ns, cudaStream_t stream) {
+                             int ratio, const uint16_t* q, int H, float scale, const float* lse, float* mass, void* ws,
+                             int num_sms, uint64_t wait_ns, cudaStream_t stream) {
   static ContextMemo attrs;
   const size_t smem = sizeof(MassSmem) + 1024;
   cudaError_t e = attrs.once([&] {
@@ -445,10 +508,11 @@ cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32
   if (e != cudaSuccess) return e;
   const DenseArgs a = {cache, q_start, q_pos, n_queries, ratio, H, 1, 1};
   const int pairs = min(kMaxPairs, num_sms / 2);
-  attn_mass_kernel<<<2 * pairs, kMThreads, smem, stream>>>(a, q_map, scale, lse, mass, ws, wait_ns);
+  attn_mass_kernel<<<2 * pairs, kMThreads, smem, stream>>>(a, reinterpret_cast<const __nv_bfloat16*>(q), scale, lse, mass,
+                                                           ws, wait_ns);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_mass_join_kernel<<<pairs, kMKeys, 0, stream>>>(cache, mass, ws);
+  attn_mass_join_kernel<<<dim3(pairs, kMPart), kMKeys, 0, stream>>>(cache, mass, ws);
   return cudaGetLastError();
 }
 

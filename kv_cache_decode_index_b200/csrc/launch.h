@@ -137,11 +137,11 @@ size_t chunk_attn_workspace_bytes();
 cudaError_t launch_chunk_attn(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
                               int ratio, const uint16_t* q, int H, float scale, uint16_t* out, float* lse, void* ws,
                               int num_sms, uint64_t wait_ns, cudaStream_t stream);
-// Attention weight of every entry; q_map: the query rows in boxes of 32 rows x 64 channels.
+// Attention weight of every entry.
 size_t attn_mass_workspace_bytes();
 cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
-                             int ratio, int H, float scale, const float* lse, float* mass, void* ws,
-                             const CUtensorMap& q_map, int num_sms, uint64_t wait_ns, cudaStream_t stream);
+                             int ratio, const uint16_t* q, int H, float scale, const float* lse, float* mass, void* ws,
+                             int num_sms, uint64_t wait_ns, cudaStream_t stream);
 
 // Eviction by weight: selection, then the kept rows to their new pages.
 size_t evict_workspace_bytes(long long num_pages);

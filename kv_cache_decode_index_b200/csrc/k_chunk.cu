@@ -354,16 +354,21 @@ __global__ void __launch_bounds__(256)
   if (c >= r.ctas || r.lo == r.tile_lo || wsp.rec[c - 1].lo > r.tile_lo) return;
   const int row = blockIdx.z * kJoinRows + (threadIdx.x & 31);
   const int ch = blockIdx.y * kJoinChannels + (threadIdx.x >> 5) * 8;
+  int last = c;                          // the last range with a part of the tile, 32 records at a look
+  for (bool more = true; more;) {
+    const int k = last + 1 + (threadIdx.x & 31);
+    const uint32_t in = __ballot_sync(0xffffffffu, k < r.ctas && wsp.rec[min(k, r.ctas - 1)].lo < r.tile_hi);
+    last += __popc(in);                  // (the records' starts ascend)
+    more = in == 0xffffffffu;
+  }
   if (row >= r.tokens * heads) return;
-  int last = c;
-  while (last + 1 < r.ctas && wsp.rec[last + 1].lo < r.tile_hi) ++last;
   // the tile's head came from range c - 1, which ended (or also began) with it
   float M = -INFINITY;
-#pragma unroll 4
+#pragma unroll 8
   for (int k = c - 1; k <= last; ++k) M = fmaxf(M, partial_of(wsp, k, k < c ? 1 : 0, tile_rows)[tile_rows * kKvDim + row]);
   const float ref = M == -INFINITY ? 0.0f : M;
   float l = 0.0f, o[8] = {};
-#pragma unroll 4
+#pragma unroll 8
   for (int k = c - 1; k <= last; ++k) {
     const float* part = partial_of(wsp, k, k < c ? 1 : 0, tile_rows);
     const float f = exp2f(part[tile_rows * kKvDim + row] - ref);

@@ -12,7 +12,7 @@
 //     a query row is 1 KB, so this is the side to stream; for single tokens it
 //     is the only one that is long.
 //   * One warp of the leader issues the MMAs into two 256-column accumulators;
-//     four warps take exp2 and the sums.
+//     eight warps (lane quarter x half of the columns) take exp2 and the sums.
 // Why a pair: shared memory gives 128 bytes a cycle.  One CTA alone would read
 // 128 (operands of M = N = 128) and write 64 (rows); the pair reads 64 and
 // writes 32 for each of its CTAs at the full MMA rate.
@@ -30,8 +30,8 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kMEpiWarps = 4, kMDeqWarps = 8;
-constexpr int kMThreads = (kMEpiWarps + kMDeqWarps + 1) * 32;   // 416
+constexpr int kMEpiWarps = 8, kMDeqWarps = 8, kMMmaWarp = kMEpiWarps + kMDeqWarps;
+constexpr int kMThreads = (kMMmaWarp + 1) * 32;   // 544
 constexpr int kMKeys = 256;                       // entries of a tile (both CTAs)
 constexpr int kMRows = 256;                       // query rows of a tile (both CTAs)
 constexpr int kMPart = 16;                        // tiles of entries whose sums a pair holds
@@ -49,7 +49,7 @@ struct __align__(1024) MassSmem {
                                                   // other CTA fills its half of the next one) ...
   float col_lse2[kMRows];                         // ... log2 of the row's sum ...
   int col_lim[kMRows];                            // ... and entries that it sees (0: no row)
-  float sum[kMPart * kMKeys / 2];                 // this CTA's entries of the part
+  float sum[2][kMPart * kMKeys / 2];              // this CTA's entries of the part, per half of the columns
   int warp_min[kMEpiWarps];
   int ctx[kMaxDenseBatch];
   long long at[kMaxDenseBatch + 1];               // steps before each request
@@ -138,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       run += __shfl_sync(0xffffffffu, v, 31);
     }
     if (lane == 0) S.at[0] = 0;
-  } else if (warp == 12) {
+  } else if (warp == kMMmaWarp) {
     tmem_alloc_pair(&S.tmem_base, kMTmemCols);
   }
   tc_fence_before();
@@ -198,9 +198,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   if (warp < kMEpiWarps) {
     // ================= query rows, exp2 and the sums =================
     const uint32_t q_full = map_rank(smem_u32(&S.q_full), 0);
-    const uint32_t tm_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int quarter = warp & 3, hc = warp >> 2, slot = quarter * 32 + lane;   // entry of this CTA's 128, half of the columns
+    const uint32_t tm_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float sign = scale < 0.0f ? -1.0f : 1.0f;
     int item = 0, b = 0, held_b = -1, held_rt = -1, loads = 0, min_lim = 0;
+    // 16 columns of an entry.  Their factors are loaded in one go before the
+    // scores are awaited; the masked form stands apart, so that no branch lies
+    // between two columns.
+    struct Columns {
+      float4 f[4], l[4];
+    };
+    auto factors = [&](int c, Columns& x) {
+      const uint32_t fs = smem_u32(&S.col_scale[loads & 1][c]), ls = smem_u32(&S.col_lse2[c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x.f[j] = ld_shared_f4(fs + j * 16);
+        x.l[j] = ld_shared_f4(ls + j * 16);
+      }
+    };
+    auto add_weights = [&](const uint32_t (&r)[16], const Columns& x, int c, int key, bool mask, float (&part)[4]) {
+      if (!mask) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          part[0] += ex2(fmaf(__uint_as_float(r[4 * j]), x.f[j].x, -x.l[j].x));
+          part[1] += ex2(fmaf(__uint_as_float(r[4 * j + 1]), x.f[j].y, -x.l[j].y));
+          part[2] += ex2(fmaf(__uint_as_float(r[4 * j + 2]), x.f[j].z, -x.l[j].z));
+          part[3] += ex2(fmaf(__uint_as_float(r[4 * j + 3]), x.f[j].w, -x.l[j].w));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int4 lim = *reinterpret_cast<const int4*>(S.col_lim + c + 4 * j);
+          part[0] += key < lim.x ? ex2(fmaf(__uint_as_float(r[4 * j]), x.f[j].x, -x.l[j].x)) : 0.0f;
+          part[1] += key < lim.y ? ex2(fmaf(__uint_as_float(r[4 * j + 1]), x.f[j].y, -x.l[j].y)) : 0.0f;
+          part[2] += key < lim.z ? ex2(fmaf(__uint_as_float(r[4 * j + 2]), x.f[j].z, -x.l[j].z)) : 0.0f;
+          part[3] += key < lim.w ? ex2(fmaf(__uint_as_float(r[4 * j + 3]), x.f[j].w, -x.l[j].w)) : 0.0f;
+        }
+      }
+    };
     bool fresh = true;                              // no part is held
     for (long long pos = lo; ok && pos < hi;) {
       const Run u = run_at(pos, b);
@@ -208,7 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       pos += u.kt1 - u.kt0;
       const int end = seen_end(u), N = columns(u), half = N / 2;
       if (fresh) {
-        for (int i = tid; i < kMPart * kMKeys / 2; i += kMEpiWarps * 32) S.sum[i] = 0.0f;
+        for (int kt = 0; kt < kMPart; ++kt) S.sum[hc][kt * (kMKeys / 2) + slot] = 0.0f;
         fresh = false;
       }
       if (u.kt0 < end) {
@@ -247,14 +282,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           if (lane == 0) S.warp_min[warp] = min_lim;
           fence_proxy_async_smem();
           named_bar_sync(kBarEpi, kMEpiWarps * 32);
-          min_lim = min(min(S.warp_min[0], S.warp_min[1]), min(S.warp_min[2], S.warp_min[3]));
+          min_lim = __reduce_min_sync(0xffffffffu, S.warp_min[lane % kMEpiWarps]);
           if (lane == 0) mbar_arrive_cluster(q_full);
           ok = mbar_wait_cluster_all(&S.scale_full, (loads - 1) & 1, wait_ns);
         }
       }
       for (int kt = u.kt0; ok && kt < end; ++kt, ++item) {
         const int k0 = (u.part + kt) * kMKeys, key0 = k0 + static_cast<int>(rank) * (kMKeys / 2);
-        const int key = key0 + tid;
+        const int key = key0 + slot;
         int page = -1;                               // of this CTA's entries
         if (key0 < u.ctx) page = cache.page_table[static_cast<long long>(u.b) * cache.max_pages_per_req + key0 / cache.page_size];
         const bool mask = min_lim < min(k0 + kMKeys, u.ctx);
@@ -264,52 +299,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t r[2][32];
-        tmem_ld_32x32b_x32(tm_lane + acc * kMRows, r[0]);
+        uint32_t r0[16], r1[16];                     // tensor-memory loads run one part ahead
+        Columns x;
+        const int cb = hc * half, ce = cb + half;    // this warp's columns (a multiple of 16)
+        const uint32_t from = tm_lane + acc * kMRows;
+        tmem_ld_32x32b_x16(from + cb, r0);
 #pragma unroll 1
-        for (int c = 0; c < N; c += 64) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c1 = c + h * 32;
-            if (c1 >= N) break;
+        for (int c = cb; c < ce; c += 32) {
+          factors(c, x);
+          tmem_ld_wait();
+          if (c + 16 < ce) tmem_ld_32x32b_x16(from + c + 16, r1);
+          add_weights(r0, x, c, key, mask, part);
+          if (c + 16 < ce) {
+            factors(c + 16, x);
             tmem_ld_wait();
-            if (c1 + 32 < N) tmem_ld_32x32b_x32(tm_lane + acc * kMRows + c1 + 32, r[h ^ 1]);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(&S.col_scale[loads & 1][c1 + j]);
-              const float4 l4 = *reinterpret_cast<const float4*>(&S.col_lse2[c1 + j]);
-              const float sv[4] = {s4.x, s4.y, s4.z, s4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-              if (mask) {
-                const int4 m4 = *reinterpret_cast<const int4*>(&S.col_lim[c1 + j]);
-                const int mv[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float p = ex2(fmaf(__uint_as_float(r[h][j + k]), sv[k], -lv[k]));
-                  part[k] += key < mv[k] ? p : 0.0f;
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) part[k] += ex2(fmaf(__uint_as_float(r[h][j + k]), sv[k], -lv[k]));
-              }
-            }
+            if (c + 32 < ce) tmem_ld_32x32b_x16(from + c + 32, r0);
+            add_weights(r1, x, c + 16, key, mask, part);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acc_empty[acc]), 0));
-        if (page >= 0 && page < cache.num_pages) S.sum[kt * (kMKeys / 2) + tid] += (part[0] + part[1]) + (part[2] + part[3]);
+        if (page >= 0 && page < cache.num_pages) S.sum[hc][kt * (kMKeys / 2) + slot] += (part[0] + part[1]) + (part[2] + part[3]);
       }
       // the part's end, or the range's: the entries' weights, or this pair's share of them
       if (ok && (pos >= hi || pos >= u.part_hi)) {
         const bool whole = u.part_lo >= lo && u.part_hi <= hi;
         float* share = wsp.part + (2 * static_cast<size_t>(pair) + (u.part_lo < lo ? 0 : 1)) * (kMPart * kMKeys);
+        named_bar_sync(kBarEpi, kMEpiWarps * 32);       // both halves of the columns
 #pragma unroll 4
-        for (int kt = 0; kt < kMPart; ++kt) {
-          const int in = kt * kMKeys + static_cast<int>(rank) * (kMKeys / 2) + tid, key = u.part * kMKeys + in;
-          const float s = S.sum[kt * (kMKeys / 2) + tid];
+        for (int kt = hc; kt < kMPart; kt += 2) {
+          const int in = kt * kMKeys + static_cast<int>(rank) * (kMKeys / 2) + slot, key = u.part * kMKeys + in;
+          const float s = S.sum[0][kt * (kMKeys / 2) + slot] + S.sum[1][kt * (kMKeys / 2) + slot];
           if (!whole) share[in] = s;
           else if (key < u.ctx && s != 0.0f) mass[u.b * capacity + key] += s;
         }
+        named_bar_sync(kBarEpi, kMEpiWarps * 32);
         fresh = true;
       }
     }
@@ -472,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();          // every MMA has completed, no barrier of the other CTA is touched after this
-  if (warp == 12) tmem_release_pair(tmem, kMTmemCols);
+  if (warp == kMMmaWarp) tmem_release_pair(tmem, kMTmemCols);
 }
 
 // Joins the parts that ranges cut: block (c, y) takes 256 entries of the part

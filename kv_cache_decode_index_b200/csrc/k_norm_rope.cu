@@ -19,34 +19,18 @@ namespace {
 constexpr int kNThreads = 256;
 constexpr int kNWarps = kNThreads / 32;
 
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+// Four consecutive elements as fp32.
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                     __uint_as_float(r.y & 0xFFFF0000u));
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
 // cos and sin of pos * freq: the angle in float64, reduced to [-pi, pi] by a
 // two-part 2 pi, then fp32 (|angle| <= pi rounded to fp32: off by <= 1.2e-7).
@@ -60,54 +44,67 @@ __device__ __forceinline__ float2 turn_of(int pos, double freq) {
   return t;
 }
 
-// A row of D elements is D / 8 chunks of 8; a group of G lanes holds a row,
-// lane g its chunks g and (D = 512) g + 32.
+// A row of D elements is D / 8 units of two groups of 4 channels; G lanes hold
+// a row, lane g its units g and (D = 512) g + 32.  A unit of the rotated part
+// holds whole pairs: the groups are 8 neighbours when pairs are interleaved or
+// nothing is rotated there, and 4 channels with their partners rot / 2 further
+// on otherwise.  So the rotation needs no exchange between lanes; with 8
+// neighbours a lane and shuffles to the partners the kernel took 32 instructions
+// an element, and twice the time.
+// Bound by memory: the row is read and written once.
 template <int D, int R, typename Tin, typename Tout>
-__global__ void __launch_bounds__(kNThreads)
+__global__ void __launch_bounds__(kNThreads, D == 128 ? 5 : 4)
     norm_rope_kernel(int n_rows, int heads, const Tin* x, long long x_stride, const float* __restrict__ weight,
                      float eps, const double* __restrict__ freqs, int rot, int interleaved,
                      const int32_t* __restrict__ pos, Tout* out, int tokens_per_block, int heads_per_block) {
-  constexpr int kChunks = D / 8;
-  constexpr int G = kChunks < 32 ? kChunks : 32;       // lanes per row
-  constexpr int C = kChunks / G;                       // chunks per lane
+  constexpr int kUnits = D / 8;
+  constexpr int G = kUnits < 32 ? kUnits : 32;         // lanes per row
+  constexpr int C = kUnits / G;                        // units per lane
   constexpr int RPW = 32 / G;                          // rows a warp holds at once
-  extern __shared__ float2 turns[];                    // [tokens_per_block][rot / 2]
+  extern __shared__ float4 turn_pairs[];               // [tokens_per_block][rot / 4] two (cos, sin) each
+  float2* turns = reinterpret_cast<float2*>(turn_pairs);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane % G;
   const int half = rot / 2, lo = D - rot;
   const int t0 = blockIdx.x * tokens_per_block, h0 = blockIdx.y * heads_per_block;
-  const int nh = min(heads_per_block, heads - h0);
-  const int rows = min(tokens_per_block, n_rows - t0) * nh;
+  const int nh = min(heads_per_block, heads - h0), nt = min(tokens_per_block, n_rows - t0);
+  const int rows = nt * nh;
+
+  // the lane's channels, the same in every row
+  int ca[C], cb[C], turn[C];                           // turn: its first pair, or -1
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int u = g + c * G;
+    ca[c] = u * 8;
+    cb[c] = u * 8 + 4;
+    turn[c] = -1;
+    if (u * 8 >= lo) {
+      turn[c] = (u * 8 - lo) / 2;
+      if (!interleaved) ca[c] = lo + turn[c], cb[c] = lo + half + turn[c];
+    }
+  }
 
   // the rows first: they do not wait for the angles
-  float v[R][C][8];
+  float4 va[R][C], vb[R][C];
   int tok[R], head[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int r = (i * kNWarps + warp) * RPW + lane / G;
-    tok[i] = r < rows ? r / nh : -1;
-    head[i] = r < rows ? h0 + r % nh : 0;
+    tok[i] = tokens_per_block == 1 ? 0 : r / nh;
+    head[i] = h0 + (tokens_per_block == 1 ? r : r % nh);
+    if (r >= rows) tok[i] = -1;
+    const Tin* src = x + static_cast<long long>(t0 + max(tok[i], 0)) * x_stride + (tok[i] < 0 ? h0 : head[i]) * D;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (tok[i] >= 0) {
-        load8(x + static_cast<long long>(t0 + tok[i]) * x_stride + static_cast<long long>(head[i]) * D + (g + c * G) * 8,
-              v[i][c]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][c][k] = 0.0f;
-      }
+      va[i][c] = load4(src + ca[c]);                   // (lanes without a row read the block's first again)
+      vb[i][c] = load4(src + cb[c]);
     }
   }
-  float w[C][8];
+  float4 wa[C], wb[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if (weight != nullptr) {
-      load8(weight + (g + c * G) * 8, w[c]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[c][k] = 1.0f;
-    }
+    wa[c] = wb[c] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (weight != nullptr) wa[c] = load4(weight + ca[c]), wb[c] = load4(weight + cb[c]);
   }
-  const int nt = min(tokens_per_block, n_rows - t0);
   for (int i = threadIdx.x; i < nt * half; i += kNThreads) turns[i] = turn_of(pos[t0 + i / half], freqs[i % half]);
   __syncthreads();
 
@@ -115,96 +112,55 @@ __global__ void __launch_bounds__(kNThreads)
   for (int i = 0; i < R; ++i) {
     float ss = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(v[i][c][k], v[i][c][k], ss);
+    for (int c = 0; c < C; ++c) {
+      const float4 a = va[i][c], b = vb[i][c];
+      ss = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(a.z, a.z, fmaf(a.w, a.w, ss))));
+      ss = fmaf(b.x, b.x, fmaf(b.y, b.y, fmaf(b.z, b.z, fmaf(b.w, b.w, ss))));
+    }
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    float inv;
-    if (ss <= 1e37f) {
-      inv = 1.0f / sqrtf(ss * (1.0f / D) + eps);
-    } else {
-      inv = 0.0f;
-    }
+    float inv = rsqrtf(fmaf(ss, 1.0f / D, eps));
     // Squares that leave fp32's range: the row times 2^-70 (every lane of the
     // warp takes part; the sum of 512 squares is then below 2^126).
     if (__any_sync(0xffffffffu, !(ss <= 1e37f))) {
       constexpr float kDown = 8.470329472543003e-22f;   // 2^-70
+      const bool big = !(ss <= 1e37f);
+      const float down = big ? kDown : 1.0f;
       float s2 = 0.0f;
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float d = v[i][c][k] * kDown;
-          s2 = fmaf(d, d, s2);
-        }
+      for (int c = 0; c < C; ++c) {
+        float4 &a = va[i][c], &b = vb[i][c];
+        a.x *= down; a.y *= down; a.z *= down; a.w *= down;
+        b.x *= down; b.y *= down; b.z *= down; b.w *= down;
+        s2 = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(a.z, a.z, fmaf(a.w, a.w, s2))));
+        s2 = fmaf(b.x, b.x, fmaf(b.y, b.y, fmaf(b.z, b.z, fmaf(b.w, b.w, s2))));
+      }
 #pragma unroll
       for (int o = G / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-      if (!(ss <= 1e37f)) {
-        inv = 1.0f / sqrtf(s2 * (1.0f / D));            // eps <= 1 is nothing next to a mean above 1e34
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[i][c][k] *= kDown;
-      }
+      if (big) inv = rsqrtf(s2 * (1.0f / D));           // eps <= 1 is nothing next to a mean above 1e34
     }
+    Tout* dst = out + (static_cast<long long>(t0 + max(tok[i], 0)) * heads + head[i]) * D;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[i][c][k] = v[i][c][k] * inv * w[c][k];
-
-    if (rot > 0) {
-      const float2* tt = turns + max(tok[i], 0) * half;
-      if (interleaved) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int ch = (g + c * G) * 8 - lo;          // first rotated channel of the chunk, if any
-          if (ch >= 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 t = tt[ch / 2 + k];
-              const float u = v[i][c][2 * k], z = v[i][c][2 * k + 1];
-              v[i][c][2 * k] = u * t.x - z * t.y;
-              v[i][c][2 * k + 1] = u * t.y + z * t.x;
-            }
-          }
-        }
-      } else {
-        // the partner chunk is rot / 16 chunks away (rot is a multiple of
-        // 32: whole chunks), in another lane or in this lane's other chunk
-        float p[C][8];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int ch = (g + c * G) * 8 - lo;
-          const int other = g + c * G + (ch < half ? half / 8 : -(half / 8));
-          const int src = ch >= 0 ? other : 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            p[c][k] = __shfl_sync(0xffffffffu, v[i][0][k], src % G, G);
-            if (C > 1) {
-              const float q = __shfl_sync(0xffffffffu, v[i][C - 1][k], src % G, G);
-              if (src >= G) p[c][k] = q;
-            }
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int ch = (g + c * G) * 8 - lo;
-          if (ch >= 0) {
-            const bool first = ch < half;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 t = tt[(first ? ch : ch - half) + k];
-              v[i][c][k] = first ? v[i][c][k] * t.x - p[c][k] * t.y : p[c][k] * t.y + v[i][c][k] * t.x;
-            }
-          }
+    for (int c = 0; c < C; ++c) {
+      float4 a = va[i][c], b = vb[i][c];
+      a.x *= inv * wa[c].x; a.y *= inv * wa[c].y; a.z *= inv * wa[c].z; a.w *= inv * wa[c].w;
+      b.x *= inv * wb[c].x; b.y *= inv * wb[c].y; b.z *= inv * wb[c].z; b.w *= inv * wb[c].w;
+      if (turn[c] >= 0) {
+        const float4* tt = reinterpret_cast<const float4*>(turns + max(tok[i], 0) * half + turn[c]);
+        const float4 p = tt[0], q = tt[1];              // (cos, sin) of four pairs
+        if (interleaved) {
+          a = make_float4(a.x * p.x - a.y * p.y, a.x * p.y + a.y * p.x, a.z * p.z - a.w * p.w, a.z * p.w + a.w * p.z);
+          b = make_float4(b.x * q.x - b.y * q.y, b.x * q.y + b.y * q.x, b.z * q.z - b.w * q.w, b.z * q.w + b.w * q.z);
+        } else {
+          const float4 u = a, v = b;
+          a = make_float4(u.x * p.x - v.x * p.y, u.y * p.z - v.y * p.w, u.z * q.x - v.z * q.y, u.w * q.z - v.w * q.w);
+          b = make_float4(u.x * p.y + v.x * p.x, u.y * p.w + v.y * p.z, u.z * q.y + v.z * q.x, u.w * q.w + v.w * q.z);
         }
       }
-    }
-    if (tok[i] >= 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        store8(out + (static_cast<long long>(t0 + tok[i]) * heads + head[i]) * D + (g + c * G) * 8, v[i][c]);
+      if (tok[i] >= 0) {
+        store4(dst + ca[c], a);
+        store4(dst + cb[c], b);
+      }
     }
   }
 }
@@ -269,22 +225,13 @@ __global__ void __launch_bounds__(128)
   if (row < 0) return;
   float x[16], k4[4];
   {
-    float a[8], b[8];
-    load8(kv + i * kv_stride + lane * 16, a);
-    load8(kv + i * kv_stride + lane * 16 + 8, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = a[j], x[8 + j] = b[j];
-    const T* kp = ik + i * ik_stride + lane * 4;
-    if constexpr (sizeof(T) == 2) {
-      const uint2 r = *reinterpret_cast<const uint2*>(kp);
-      k4[0] = __uint_as_float(r.x << 16);
-      k4[1] = __uint_as_float(r.x & 0xFFFF0000u);
-      k4[2] = __uint_as_float(r.y << 16);
-      k4[3] = __uint_as_float(r.y & 0xFFFF0000u);
-    } else {
-      const float4 r = *reinterpret_cast<const float4*>(kp);
-      k4[0] = r.x; k4[1] = r.y; k4[2] = r.z; k4[3] = r.w;
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = load4(kv + i * kv_stride + lane * 16 + 4 * j);
+      x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
     }
+    const float4 r = load4(ik + i * ik_stride + lane * 4);
+    k4[0] = r.x; k4[1] = r.y; k4[2] = r.z; k4[3] = r.w;
   }
   // angles of this row, spread over the lanes
   double2* tkv = turn_tab + wib * ((kv_rope.rot + ik_rope.rot) / 2);
@@ -367,8 +314,12 @@ cudaError_t launch_nr_types(int n_rows, int heads, const void* x, csa2_dtype xt,
 cudaError_t launch_norm_rope(int n_rows, int heads, int dim, const void* x, csa2_dtype x_type, long long x_stride,
                              const float* weight, float eps, const csa2_rope& rope, const int32_t* pos, void* out,
                              csa2_dtype out_type, cudaStream_t stream) {
+  // Rows a warp holds at once: two where there are rows enough to fill the GPU
+  // with such blocks, else one.
+  const bool many = static_cast<long long>(n_rows) * heads * dim >= (1LL << 22);
   if (dim == 128)
-    return launch_nr_types<128, 1>(n_rows, heads, x, x_type, x_stride, weight, eps, rope, pos, out, out_type, stream);
+    return many ? launch_nr_types<128, 2>(n_rows, heads, x, x_type, x_stride, weight, eps, rope, pos, out, out_type, stream)
+                : launch_nr_types<128, 1>(n_rows, heads, x, x_type, x_stride, weight, eps, rope, pos, out, out_type, stream);
   return launch_nr_types<512, 1>(n_rows, heads, x, x_type, x_stride, weight, eps, rope, pos, out, out_type, stream);
 }
 

@@ -22,6 +22,21 @@ __device__ __forceinline__ long long row_of(const csa2_cache& cache, int b, int 
   return static_cast<long long>(page) * cache.page_size + t % cache.page_size;
 }
 
+// What a lane stores of a row: 16 E2M1 codes (8 bytes) and their scale code, 4
+// E4M3 indexer codes and the row's exponent.
+struct PackedRow {
+  uint2 kv;
+  uint32_t kv_scale;
+  uint32_t ik;
+  int ik_exp;
+};
+__device__ __forceinline__ void store_row(const csa2_cache& cache, long long row, const PackedRow& p, int lane) {
+  reinterpret_cast<uint2*>(cache.kv_codes + row * kKvCodeBytes)[lane] = p.kv;
+  cache.kv_scales[row * kKvScaleBytes + lane] = static_cast<uint8_t>(p.kv_scale);
+  reinterpret_cast<uint32_t*>(cache.ik_codes + row * kIndexDim)[lane] = p.ik;
+  if (lane == 0) cache.ik_exp[row] = static_cast<uint8_t>(p.ik_exp + 127);
+}
+
 // Quantise one row held by a warp and store it: x = main-KV channels
 // 16*lane .. 16*lane+15, k = indexer-K elements 4*lane .. 4*lane+3.
 __device__ __forceinline__ void quantize_store(const csa2_cache& cache, long long row, const float (&x)[16], float4 k,
@@ -40,8 +55,6 @@ __device__ __forceinline__ void quantize_store(const csa2_cache& cache, long lon
       else hi |= byte << (8 * (i - 4));
     }
   }
-  reinterpret_cast<uint2*>(cache.kv_codes + row * kKvCodeBytes)[lane] = make_uint2(lo, hi);
-  cache.kv_scales[row * kKvScaleBytes + lane] = static_cast<uint8_t>(sc);
 
   float km = fmaxf(fmaxf(fabsf(k.x), fabsf(k.y)), fmaxf(fabsf(k.z), fabsf(k.w)));
 #pragma unroll
@@ -49,19 +62,22 @@ __device__ __forceinline__ void quantize_store(const csa2_cache& cache, long lon
   const int e = indexer_exponent(km);
   const float inv = exp2i(-e);
   const uint32_t codes = e4m3x2(k.x * inv, k.y * inv) | (e4m3x2(k.z * inv, k.w * inv) << 16);
-  reinterpret_cast<uint32_t*>(cache.ik_codes + row * kIndexDim)[lane] = codes;
-  if (lane == 0) cache.ik_exp[row] = static_cast<uint8_t>(e + 127);
+  store_row(cache, row, PackedRow{make_uint2(lo, hi), sc, codes, e}, lane);
 }
 
 // Quantise one indexer key held by a warp (k = elements 4*lane .. 4*lane+3)
 // to the FP4 indexer format and store it in row `row`.
-__device__ __forceinline__ void store_ik4(uint8_t* codes, uint8_t* scales, long long row, float4 k, int lane) {
-  uint32_t sc;
-  const uint32_t c = fp4_row_lane(k, &sc);
+__device__ __forceinline__ void store_ik4_codes(uint8_t* codes, uint8_t* scales, long long row, uint32_t c, uint32_t sc,
+                                                int lane) {
   reinterpret_cast<uint16_t*>(codes + row * CSA2_IK4_CODE_BYTES)[lane] = static_cast<uint16_t>(c);
   if ((lane & 3) == 0)
     scales[(row / kTile) * CSA2_IK4_TILE_SCALE_BYTES +
            block_scale_offset(static_cast<uint32_t>(row % kTile), lane >> 2)] = static_cast<uint8_t>(sc);
+}
+__device__ __forceinline__ void store_ik4(uint8_t* codes, uint8_t* scales, long long row, float4 k, int lane) {
+  uint32_t sc;
+  const uint32_t c = fp4_row_lane(k, &sc);
+  store_ik4_codes(codes, scales, row, c, sc, lane);
 }
 
 }  // namespace csa2

@@ -166,10 +166,7 @@ __global__ void __launch_bounds__(kNThreads, D == 128 ? 5 : 4)
 }
 
 // New cache rows: one warp per row, lane l holding main-KV channels 16l .. 16l+15
-// and indexer elements 4l .. 4l+3 (the layout of quantize_store).  Everything
-// up to the rounding to fp32 is float64, so that the stored codes are those of
-// the formula itself: an fp32 norm, off by 1e-7, would move values across the
-// FP4 and FP8 borders.
+// and indexer elements 4l .. 4l+3 (the layout of quantize_store).
 __device__ __forceinline__ double warp_sum(double s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -212,45 +209,37 @@ __device__ __forceinline__ void rotate_lane(double (&y)[N], int lane, int rot, b
 }
 
 template <typename T>
-__global__ void __launch_bounds__(128)
-    norm_rope_append_kernel(csa2_cache cache, uint8_t* ik4_codes, uint8_t* ik4_scales, int n_rows, const T* kv,
-                            long long kv_stride, const T* ik, long long ik_stride, const float* kv_weight,
-                            const float* ik_weight, double eps, RopeArg kv_rope, RopeArg ik_rope, int kv_inter,
-                            int ik_inter, const int32_t* rope_pos, const int32_t* req, const int32_t* pos) {
-  extern __shared__ double2 turn_tab[];               // per warp: [kv_rot / 2] then [ik_rot / 2]
-  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * (blockDim.x >> 5) + wib;
-  if (i >= n_rows) return;
-  const long long row = row_of(cache, req ? req[i] : i, pos[i], lane);
-  if (row < 0) return;
-  float x[16], k4[4];
-  {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = load4(kv + i * kv_stride + lane * 16 + 4 * j);
-      x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
-    }
-    const float4 r = load4(ik + i * ik_stride + lane * 4);
-    k4[0] = r.x; k4[1] = r.y; k4[2] = r.z; k4[3] = r.w;
-  }
-  // angles of this row, spread over the lanes
-  double2* tkv = turn_tab + wib * ((kv_rope.rot + ik_rope.rot) / 2);
-  const bool same = kv_rope.freqs == ik_rope.freqs && kv_rope.rot == ik_rope.rot;
-  double2* tik = same ? tkv : tkv + kv_rope.rot / 2;
-  const double p = static_cast<double>(rope_pos ? rope_pos[i] : pos[i]);
-  for (int f = lane; f < kv_rope.rot / 2; f += 32) {
-    double2 t;
-    sincos(p * kv_rope.freqs[f], &t.y, &t.x);
-    tkv[f] = t;
-  }
-  if (!same)
-    for (int f = lane; f < ik_rope.rot / 2; f += 32) {
-      double2 t;
-      sincos(p * ik_rope.freqs[f], &t.y, &t.x);
-      tik[f] = t;
-    }
-  __syncwarp();
+struct AppendArgs {
+  csa2_cache cache;
+  uint8_t *ik4_codes, *ik4_scales;
+  int n_rows;
+  const T *kv, *ik;
+  long long kv_stride, ik_stride;
+  const float *kv_weight, *ik_weight;
+  double eps;
+  RopeArg kv_rope, ik_rope;
+  int kv_inter, ik_inter;
+  const int32_t *rope_pos, *req, *pos;
+};
 
+// Row i in float64, as it is defined, into cache row `row`; tab: shared memory
+// for (rot + rot) / 2 (cos, sin) pairs of this warp.
+template <typename T>
+__device__ __noinline__ void append_exact(const AppendArgs<T>& a, int i, long long row, int lane, double2* tab) {
+  float x[16], k4[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = load4(a.kv + i * a.kv_stride + lane * 16 + 4 * j);
+    x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+  }
+  const float4 r = load4(a.ik + i * a.ik_stride + lane * 4);
+  k4[0] = r.x; k4[1] = r.y; k4[2] = r.z; k4[3] = r.w;
+  double2 *tkv = tab, *tik = tab + a.kv_rope.rot / 2;
+  const double p = static_cast<double>(a.rope_pos ? a.rope_pos[i] : a.pos[i]);
+  __syncwarp();
+  for (int f = lane; f < a.kv_rope.rot / 2; f += 32) sincos(p * a.kv_rope.freqs[f], &tkv[f].y, &tkv[f].x);
+  for (int f = lane; f < a.ik_rope.rot / 2; f += 32) sincos(p * a.ik_rope.freqs[f], &tik[f].y, &tik[f].x);
+  __syncwarp();
   double y[16], z[4], s = 0.0, sk = 0.0;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -262,26 +251,212 @@ __global__ void __launch_bounds__(128)
     z[j] = static_cast<double>(k4[j]);
     sk = fma(z[j], z[j], sk);
   }
-  const double inv = 1.0 / sqrt(warp_sum(s) * (1.0 / kKvDim) + eps);
-  const double invk = 1.0 / sqrt(warp_sum(sk) * (1.0 / kIndexDim) + eps);
+  const double inv = 1.0 / sqrt(warp_sum(s) * (1.0 / kKvDim) + a.eps);
+  const double invk = 1.0 / sqrt(warp_sum(sk) * (1.0 / kIndexDim) + a.eps);
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     y[j] *= inv;
-    if (kv_weight) y[j] *= static_cast<double>(kv_weight[lane * 16 + j]);
+    if (a.kv_weight) y[j] *= static_cast<double>(a.kv_weight[lane * 16 + j]);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     z[j] *= invk;
-    if (ik_weight) z[j] *= static_cast<double>(ik_weight[lane * 4 + j]);
+    if (a.ik_weight) z[j] *= static_cast<double>(a.ik_weight[lane * 4 + j]);
   }
-  if (kv_rope.rot > 0) rotate_lane<16, kKvDim>(y, lane, kv_rope.rot, kv_inter != 0, tkv);
-  if (ik_rope.rot > 0) rotate_lane<4, kIndexDim>(z, lane, ik_rope.rot, ik_inter != 0, tik);
+  if (a.kv_rope.rot > 0) rotate_lane<16, kKvDim>(y, lane, a.kv_rope.rot, a.kv_inter != 0, tkv);
+  if (a.ik_rope.rot > 0) rotate_lane<4, kIndexDim>(z, lane, a.ik_rope.rot, a.ik_inter != 0, tik);
 #pragma unroll
   for (int j = 0; j < 16; ++j) x[j] = __double2float_rn(y[j]);
   const float4 k = make_float4(__double2float_rn(z[0]), __double2float_rn(z[1]), __double2float_rn(z[2]),
                                __double2float_rn(z[3]));
-  quantize_store(cache, row, x, k, lane);
-  if (ik4_codes != nullptr) store_ik4(ik4_codes, ik4_scales, row, k, lane);
+  quantize_store(a.cache, row, x, k, lane);
+  if (a.ik4_codes != nullptr) store_ik4(a.ik4_codes, a.ik4_scales, row, k, lane);
+}
+
+// fp32 form of a lane's N channels of a row of D: y = x * inv * w, rotated, and
+// a bound of |y - its exact value| for each.  fp32 errors, in 2^-24: the sum of
+// squares 16 terms a lane and 5 steps (21, halved by the root), eps and mean 2,
+// rsqrtf 4, products 2; the rotation's cos and sin 5.2 and its product and sum
+// 2, of |u| + |v|: below 26.  64 (2^-18) are allowed for; the rounding to fp32 of
+// the exact value is one of them.
+constexpr float kAppendErr = 3.814697265625e-06f;   // 2^-18
+template <int N, int D>
+__device__ __forceinline__ void rotate_fast(float (&y)[N], float (&err)[N], int lane, int rot, bool interleaved,
+                                            const float2* tt) {
+  const int half = rot / 2, ch = lane * N - (D - rot);
+#pragma unroll
+  for (int k = 0; k < N; ++k) err[k] = fabsf(y[k]);
+  if (rot > 0) {
+    if (interleaved) {
+      if (ch >= 0) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+          const float2 t = tt[ch / 2 + k];
+          const float u = y[2 * k], v = y[2 * k + 1];
+          y[2 * k] = u * t.x - v * t.y;
+          y[2 * k + 1] = u * t.y + v * t.x;
+          err[2 * k] = err[2 * k + 1] = fabsf(u) + fabsf(v);
+        }
+      }
+    } else {
+      const bool first = ch < half;
+      const int src = ch >= 0 ? lane + (first ? half / N : -(half / N)) : lane;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float p = __shfl_sync(0xffffffffu, y[k], src);
+        if (ch >= 0) {
+          const float2 t = tt[(first ? ch : ch - half) + k];
+          err[k] = fabsf(y[k]) + fabsf(p);
+          y[k] = first ? y[k] * t.x - p * t.y : p * t.y + y[k] * t.x;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) err[k] *= kAppendErr;
+}
+
+// Eight E2M1 codes of v / s (r: about 1 / s), -0 as +0.
+__device__ __forceinline__ uint32_t e2m1x8(const float* v, float r) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t b;
+    asm("{\n\t.reg .b8 c;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
+        "cvt.u32.u8 %0, c;\n\t}"
+        : "=r"(b)
+        : "f"(v[2 * i + 1] * r), "f"(v[2 * i] * r));
+    w |= b << (8 * i);
+  }
+  const uint32_t some = ((w & 0x77777777u) + 0x77777777u) & 0x88888888u;   // sign bits of codes that are not 0
+  return w & (some | 0x77777777u);
+}
+
+// The stored codes are those of the float64 formula rounded once to fp32: an
+// fp32 norm, off by 1e-7, would now and then move a value across an FP4 or FP8
+// border.  float64 for every row is slow (conversions run at an eighth of the
+// fp32 rate: 63 us for 32,765 rows), and rarely needed: the quantisation is
+// monotone, so when y - err and y + err, the ends of the interval that holds
+// the exact value, give the same scales, exponents and codes, these are the
+// exact value's.  Rows where they differ (about one in 60), and rows outside
+// fp32's comfortable range, take append_exact.
+template <typename T>
+__global__ void __launch_bounds__(128, 6) norm_rope_append_kernel(const __grid_constant__ AppendArgs<T> a) {
+  extern __shared__ double2 turn_tab[];               // per warp: (kv rot + ik rot) / 2 entries
+  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * (blockDim.x >> 5) + wib;
+  if (i >= a.n_rows) return;
+  float y[16], z[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = load4(a.kv + i * a.kv_stride + lane * 16 + 4 * j);
+    y[4 * j] = v.x; y[4 * j + 1] = v.y; y[4 * j + 2] = v.z; y[4 * j + 3] = v.w;
+  }
+  {
+    const float4 v = load4(a.ik + i * a.ik_stride + lane * 4);
+    z[0] = v.x; z[1] = v.y; z[2] = v.z; z[3] = v.w;
+  }
+  const long long row = row_of(a.cache, a.req ? a.req[i] : i, a.pos[i], lane);
+  // angles of this row, spread over the lanes
+  double2* tab = turn_tab + wib * ((a.kv_rope.rot + a.ik_rope.rot) / 2);
+  float2 *tkv = reinterpret_cast<float2*>(tab), *tik = tkv;
+  const int rope_pos = a.rope_pos ? a.rope_pos[i] : a.pos[i];
+  for (int f = lane; f < a.kv_rope.rot / 2; f += 32) tkv[f] = turn_of(rope_pos, a.kv_rope.freqs[f]);
+  if (a.kv_rope.freqs != a.ik_rope.freqs || a.kv_rope.rot != a.ik_rope.rot) {
+    tik = tkv + a.kv_rope.rot / 2;
+    for (int f = lane; f < a.ik_rope.rot / 2; f += 32) tik[f] = turn_of(rope_pos, a.ik_rope.freqs[f]);
+  }
+  __syncwarp();
+  if (row < 0) return;
+
+  float s = 0.0f, sk = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) s = fmaf(y[j], y[j], s);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sk = fmaf(z[j], z[j], sk);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    sk += __shfl_xor_sync(0xffffffffu, sk, o);
+  }
+  const float eps = static_cast<float>(a.eps);
+  const float inv = rsqrtf(fmaf(s, 1.0f / kKvDim, eps)), invk = rsqrtf(fmaf(sk, 1.0f / kIndexDim, eps));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (a.kv_weight) w = load4(a.kv_weight + lane * 16 + 4 * j);
+    y[4 * j] *= inv * w.x; y[4 * j + 1] *= inv * w.y; y[4 * j + 2] *= inv * w.z; y[4 * j + 3] *= inv * w.w;
+  }
+  {
+    float4 w = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (a.ik_weight) w = load4(a.ik_weight + lane * 4);
+    z[0] *= invk * w.x; z[1] *= invk * w.y; z[2] *= invk * w.z; z[3] *= invk * w.w;
+  }
+  float ey[16], ez[4];
+  rotate_fast<16, kKvDim>(y, ey, lane, a.kv_rope.rot, a.kv_inter != 0, tkv);
+  rotate_fast<4, kIndexDim>(z, ez, lane, a.ik_rope.rot, a.ik_inter != 0, tik);
+
+  // main KV: both ends' scale and codes
+  float lo16[16], hi16[16], amax_lo = 0.0f, amax_hi = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    amax_lo = fmaxf(amax_lo, fabsf(y[j]) - ey[j]);
+    amax_hi = fmaxf(amax_hi, fabsf(y[j]) + ey[j]);
+    lo16[j] = y[j] - ey[j];
+    hi16[j] = y[j] + ey[j];
+  }
+  PackedRow p;
+  p.kv_scale = e4m3_code_of_sixth(amax_hi);
+  bool sure = p.kv_scale == e4m3_code_of_sixth(amax_lo);
+  p.kv = make_uint2(0u, 0u);
+  if (p.kv_scale != 0u) {
+    const float r = 1.0f / e4m3_value(p.kv_scale);   // off by 2^-24, as is its product: within err's reserve
+    p.kv = make_uint2(e2m1x8(lo16, r), e2m1x8(lo16 + 8, r));
+    sure = sure && p.kv.x == e2m1x8(hi16, r) && p.kv.y == e2m1x8(hi16 + 8, r);
+  }
+  // indexer key
+  float km_lo = 0.0f, km_hi = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    km_lo = fmaxf(km_lo, fabsf(z[j]) - ez[j]);
+    km_hi = fmaxf(km_hi, fabsf(z[j]) + ez[j]);
+  }
+  float group_lo = km_lo, group_hi = km_hi;          // of 16 elements (4 lanes), for the FP4 form
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    km_lo = fmaxf(km_lo, __shfl_xor_sync(0xffffffffu, km_lo, o));
+    km_hi = fmaxf(km_hi, __shfl_xor_sync(0xffffffffu, km_hi, o));
+    if (o == 2) group_lo = km_lo, group_hi = km_hi;
+  }
+  p.ik_exp = indexer_exponent(km_hi);
+  sure = sure && p.ik_exp == indexer_exponent(fmaxf(km_lo, 0.0f));
+  const float two = exp2i(-p.ik_exp);
+  p.ik = e4m3x2((z[0] - ez[0]) * two, (z[1] - ez[1]) * two) | (e4m3x2((z[2] - ez[2]) * two, (z[3] - ez[3]) * two) << 16);
+  sure = sure && p.ik == (e4m3x2((z[0] + ez[0]) * two, (z[1] + ez[1]) * two) |
+                          (e4m3x2((z[2] + ez[2]) * two, (z[3] + ez[3]) * two) << 16));
+  uint32_t c4 = 0u, s4 = 0u;
+  if (a.ik4_codes != nullptr) {
+    s4 = e4m3_code_of_sixth(group_hi);
+    sure = sure && s4 == e4m3_code_of_sixth(group_lo);
+    if (s4 != 0u) {
+      const float r = 1.0f / e4m3_value(s4);
+      const float v[8] = {z[0] - ez[0], z[1] - ez[1], z[2] - ez[2], z[3] - ez[3],
+                          z[0] + ez[0], z[1] + ez[1], z[2] + ez[2], z[3] + ez[3]};
+      const uint32_t both = e2m1x8(v, r);
+      c4 = both & 0xFFFFu;
+      sure = sure && c4 == both >> 16;
+    }
+  }
+  // squares outside [1e-30, 1e30] or not finite: fp32 may have lost them
+  const bool usual = s <= 1e30f && sk <= 1e30f && (s >= 1e-20f || s == 0.0f) && (sk >= 1e-20f || sk == 0.0f) &&
+                     km_hi <= 1e30f && amax_hi <= 1e30f;
+  if (__all_sync(0xffffffffu, sure && usual)) {
+    store_row(a.cache, row, p, lane);
+    if (a.ik4_codes != nullptr) store_ik4_codes(a.ik4_codes, a.ik4_scales, row, c4, s4, lane);
+  } else {
+    append_exact(a, i, row, lane, tab);
+  }
 }
 
 template <int D, int R, typename Tin, typename Tout>
@@ -334,14 +509,17 @@ cudaError_t launch_norm_rope_append(const csa2_cache& cache, const csa2_ik4* ik4
   const RopeArg kr = {kv_rope.freqs, kv_rope.rot}, ir = {ik_rope.freqs, ik_rope.rot};
   uint8_t* c4 = ik4 ? ik4->codes : nullptr;
   uint8_t* s4 = ik4 ? ik4->scales : nullptr;
-  if (type == CSA2_BF16)
-    norm_rope_append_kernel<__nv_bfloat16><<<blocks, kWarps * 32, smem, stream>>>(
-        cache, c4, s4, n_rows, static_cast<const __nv_bfloat16*>(kv), kv_stride, static_cast<const __nv_bfloat16*>(ik),
-        ik_stride, kv_weight, ik_weight, eps, kr, ir, kv_rope.interleaved, ik_rope.interleaved, rope_pos, req, pos);
-  else
+  if (type == CSA2_BF16) {
+    using T = __nv_bfloat16;
+    norm_rope_append_kernel<T><<<blocks, kWarps * 32, smem, stream>>>(
+        AppendArgs<T>{cache, c4, s4, n_rows, static_cast<const T*>(kv), static_cast<const T*>(ik), kv_stride, ik_stride,
+                      kv_weight, ik_weight, eps, kr, ir, kv_rope.interleaved, ik_rope.interleaved, rope_pos, req, pos});
+  } else {
     norm_rope_append_kernel<float><<<blocks, kWarps * 32, smem, stream>>>(
-        cache, c4, s4, n_rows, static_cast<const float*>(kv), kv_stride, static_cast<const float*>(ik), ik_stride,
-        kv_weight, ik_weight, eps, kr, ir, kv_rope.interleaved, ik_rope.interleaved, rope_pos, req, pos);
+        AppendArgs<float>{cache, c4, s4, n_rows, static_cast<const float*>(kv), static_cast<const float*>(ik), kv_stride,
+                          ik_stride, kv_weight, ik_weight, eps, kr, ir, kv_rope.interleaved, ik_rope.interleaved, rope_pos,
+                          req, pos});
+  }
   return cudaGetLastError();
 }
 

@@ -10,8 +10,9 @@
 // threshold is exact, and the entries on it are taken from the lowest index
 // on.  Each warp then counts and emits a consecutive part, so the output is
 // sorted without a sort and without atomics whose order could show.  The
-// weights are read five times, from L2 after the first.
-// Moving: a warp per 8 rows, 417 bytes each, four rows' loads in flight.
+// weights are read once into shared memory where a CTA's part fits (up to 163,840
+// entries a request), else five times, from L2 after the first.
+// Moving: a warp per 8 rows, 417 bytes each, all their loads in flight.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -27,6 +28,7 @@ constexpr int kEThreads = 1024;
 constexpr int kEWarps = kEThreads / 32;
 constexpr int kECluster = 8;
 constexpr int kEBins = 2048;
+constexpr int kEKeys = 20480;            // 80 KB: two CTAs per SM
 constexpr int kMarkSource = 1 << 30;     // page marks: holds visible entries; below: uses as destination
 
 // Order key of a weight: larger weight, larger key; NaN above everything, and
@@ -41,6 +43,7 @@ struct EvictSmem {
   int warp_a[kEWarps], warp_b[kEWarps];
   int above, digit;          // of the pass's threshold bin
   int gt, eq;                // of this CTA's entries
+  uint32_t keys[kEKeys];     // this CTA's order keys, when they fit
 };
 
 // Exclusive prefix sums of a and b over the block's threads.
@@ -73,7 +76,8 @@ __global__ void __cluster_dims__(kECluster, 1, 1) __launch_bounds__(kEThreads)
     evict_select_kernel(const csa2_cache cache, const float* __restrict__ mass, int budget, int sink, int recent,
                         const int32_t* __restrict__ dst_pages, int dst_width, int32_t* __restrict__ kept,
                         int32_t* __restrict__ new_len, int32_t* __restrict__ marks) {
-  __shared__ EvictSmem S;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  EvictSmem& S = *reinterpret_cast<EvictSmem*>(smem_raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank());
   const int b = blockIdx.x / kECluster;
@@ -118,6 +122,13 @@ __global__ void __cluster_dims__(kECluster, 1, 1) __launch_bounds__(kEThreads)
   const int ws = ((per + kEWarps - 1) / kEWarps + 31) & ~31;   // entries per warp
   const int w0 = min(c0 + warp * ws, c1), w1 = min(w0 + ws, c1);
   const float* m = mass + b * capacity;
+  const bool cached = per <= kEKeys;
+  if (cached) {
+#pragma unroll 4
+    for (int i = c0 + tid; i < c1; i += kEThreads) S.keys[i - c0] = weight_key(m[i]);
+    __syncthreads();
+  }
+  auto key_of = [&](int i) { return cached ? S.keys[i - c0] : weight_key(m[i]); };
 
   uint32_t prefix = 0u, mask = 0u;
   int need = want;                                      // still to take among the keys on the prefix
@@ -126,19 +137,11 @@ __global__ void __cluster_dims__(kECluster, 1, 1) __launch_bounds__(kEThreads)
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
     uint32_t* hist = S.hist[pass];
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = i0 + j * 32 + lane < w1 ? m[i0 + j * 32 + lane] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t k = weight_key(v[j]);
-        const bool in = i0 + j * 32 + lane < w1 && (k & mask) == prefix;
-        // lanes of one bin count together: weights crowd (entries without any)
-        const uint32_t d = in ? (k >> shift) & digits : 0xFFFFFFFFu;
-        const uint32_t peers = __match_any_sync(0xffffffffu, d);
-        if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[d], __popc(peers));
-      }
+    // (the hardware adds up the lanes of one bin: weights crowd, entries without any most of all)
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint32_t k = key_of(i);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digits], 1u);
     }
     cluster.sync();                                     // every CTA's bins are counted
     // thread t: bins 2047 - 2t and 2046 - 2t of all CTAs, from the top down
@@ -162,16 +165,11 @@ __global__ void __cluster_dims__(kECluster, 1, 1) __launch_bounds__(kEThreads)
 
   // ---- counts of this warp's part: above the threshold, and on it ----
   int gt = 0, eq = 0;
-  for (int i0 = w0; i0 < w1; i0 += 128) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * 32 + lane;
-      if (i < w1) {
-        const uint32_t k = weight_key(m[i]);
-        gt += k > prefix;
-        eq += k == prefix;
-      }
-    }
+#pragma unroll 4
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = key_of(i);
+    gt += k > prefix;
+    eq += k == prefix;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -187,9 +185,10 @@ __global__ void __cluster_dims__(kECluster, 1, 1) __launch_bounds__(kEThreads)
     gt_before += o->gt;
     eq_before += o->eq;
   }
+#pragma unroll 4
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const int i = i0 + lane;
-    const uint32_t k = i < w1 ? weight_key(m[i]) : 0u;
+    const uint32_t k = i < w1 ? key_of(i) : 0u;
     const uint32_t g = __ballot_sync(0xffffffffu, i < w1 && k > prefix);
     const uint32_t e = __ballot_sync(0xffffffffu, i < w1 && k == prefix);
     const uint32_t below = (1u << lane) - 1u;
@@ -253,15 +252,14 @@ __global__ void __launch_bounds__(kMoveThreads)
   else if (lane < 18) base = cache.kv_scales + (lane - 16) * 16, stride = kKvScaleBytes;
   else if (lane < 26) base = cache.ik_codes + (lane - 18) * 16, stride = kIndexDim;
   else if (lane >= 28 && ik4_codes != nullptr) base = ik4_codes + (lane - 28) * 16, stride = CSA2_IK4_CODE_BYTES;
+  {
+    uint4 v[kMoveRows];
+    uint32_t x[kMoveRows];
+    int s[kMoveRows], d[kMoveRows];
 #pragma unroll
-  for (int r0 = 0; r0 < kMoveRows; r0 += 4) {
-    uint4 v[4];
-    uint32_t x[4];
-    int s[4], d[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      s[r] = __shfl_sync(0xffffffffu, src, r0 + r);
-      d[r] = __shfl_sync(0xffffffffu, dst, r0 + r);
+    for (int r = 0; r < kMoveRows; ++r) {
+      s[r] = __shfl_sync(0xffffffffu, src, r);
+      d[r] = __shfl_sync(0xffffffffu, dst, r);
       if (s[r] < 0 || d[r] < 0) continue;
       if (base != nullptr) v[r] = *reinterpret_cast<const uint4*>(base + static_cast<long long>(s[r]) * stride);
       if (lane == 26) x[r] = cache.ik_exp[s[r]];
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(kMoveThreads)
                                                   block_scale_offset(s[r] % kTile, lane * 4));
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < kMoveRows; ++r) {
       if (s[r] < 0 || d[r] < 0) continue;
       if (base != nullptr) *reinterpret_cast<uint4*>(base + static_cast<long long>(d[r]) * stride) = v[r];
       if (lane == 26) cache.ik_exp[d[r]] = static_cast<uint8_t>(x[r]);
@@ -289,11 +287,18 @@ size_t evict_workspace_bytes(long long num_pages) { return (static_cast<size_t>(
 cudaError_t launch_evict(const csa2_cache& cache, const csa2_ik4* ik4, const float* mass, int budget, int sink, int recent,
                          const int32_t* dst_pages, int dst_width, int32_t* kept, int32_t* new_len, float* mass_out,
                          void* ws, cudaStream_t stream) {
-  int32_t* marks = static_cast<int32_t*>(ws);
-  cudaError_t e = cudaMemsetAsync(marks, 0, static_cast<size_t>(cache.num_pages) * 4, stream);
+  static ContextMemo attrs;
+  cudaError_t e = attrs.once([&] {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(sizeof(EvictSmem)));
+  });
   if (e != cudaSuccess) return e;
-  evict_select_kernel<<<cache.batch * kECluster, kEThreads, 0, stream>>>(cache, mass, budget, sink, recent, dst_pages,
-                                                                         dst_width, kept, new_len, marks);
+  int32_t* marks = static_cast<int32_t*>(ws);
+  e = cudaMemsetAsync(marks, 0, static_cast<size_t>(cache.num_pages) * 4, stream);
+  if (e != cudaSuccess) return e;
+  evict_select_kernel<<<cache.batch * kECluster, kEThreads, sizeof(EvictSmem), stream>>>(cache, mass, budget, sink, recent,
+                                                                                       dst_pages, dst_width, kept, new_len,
+                                                                                       marks);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int groups = (budget + kMoveRows - 1) / kMoveRows;

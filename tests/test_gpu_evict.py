@@ -216,3 +216,19 @@ def test_evict_long_request(csa2):
     want = plain_kept(mass[0].cpu().numpy(), n, budget, 100, 5000)
     np.testing.assert_array_equal(kept[0].cpu().numpy(), want)
     assert torch.equal(cache.kv_codes[n:], cache.kv_codes[torch.from_numpy(want).cuda()])
+
+
+def test_evict_many_requests(csa2):
+    """40 requests , short and long ones among them."""
+    rng = np.random.default_rng(12)
+    lens = [int(x) for x in rng.integers(1, 3000, 40)]
+    lens[7], lens[30] = 70000, 59000
+    budget, page = 700, 128
+    cache, table, dst, k4, rng = _setup(csa2, lens, budget, page, 4)
+    mass = np.floor(np.exp(3 * rng.standard_normal((40, cache.capacity)))).astype(np.float32)
+    before = _rows(csa2, cache, k4)
+    mass_out = torch.full((40, dst.shape[1] * page), 7.0).cuda()
+    kept, new_len = csa2.evict(cache, torch.from_numpy(mass).cuda(), budget, torch.from_numpy(dst).cuda(), sink=3,
+                               recent=99, mass_out=mass_out)
+    assert csa2.get_error(cache)[0] == csa2.OK
+    _check(csa2, cache, table, dst, k4, mass, before, kept, new_len, mass_out, lens, budget, 3, 99)

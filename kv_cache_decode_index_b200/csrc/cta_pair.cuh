@@ -31,11 +31,21 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Four words of shared memory, in program order with other volatile loads.
-__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
+// Descriptor of a K-major operand stored as rows of 32 bytes with the 32-byte
+// swizzle (16-byte chunk c of row r lives at chunk c ^ ((r / 4) % 2)); 8-row
+// groups are 256 bytes apart.
+__device__ __forceinline__ uint64_t sw32_kmajor_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);   // start address
+  d |= static_cast<uint64_t>(1) << 16;                        // LBO (unused here)
+  d |= static_cast<uint64_t>(256 >> 4) << 32;                 // SBO: 8 rows x 32 B
+  d |= static_cast<uint64_t>(1) << 46;                        // descriptor version
+  d |= static_cast<uint64_t>(6) << 61;                        // 32-byte swizzle
+  return d;
+}
+// Byte offset of (row, byte c) in a 32-byte-swizzled tile of 32-byte rows.
+__host__ __device__ __forceinline__ uint32_t sw32_offset(uint32_t row, uint32_t c) {
+  return row * 32u + ((((c >> 4) ^ (row >> 2)) & 1u) << 4) + (c & 15u);
 }
 
 // 32 lanes x 16 consecutive columns of tensor memory.

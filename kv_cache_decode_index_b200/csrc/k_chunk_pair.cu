@@ -160,10 +160,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int rows = T.tokens * a.heads;           // of the pair
       const int own = static_cast<int>(rank) * kGRows + row;
       const int lim = own < rows ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : 0;
-      load_query_rows<kGRows, kGSoftWarps>(q, static_cast<long long>(T.q0) * a.heads + static_cast<int>(rank) * kGRows,
+      load_query_rows<kGRows, kGSoftWarps, kPerRow>(q, static_cast<long long>(T.q0) * a.heads + static_cast<int>(rank) * kGRows,
                                            rows - static_cast<int>(rank) * kGRows, kGRows, sign, S.q[0], warp, lane,
-                                           [&](int r, float down) {
-                                             S.row_scale[r] = fabsf(scale) * down * kLog2e * kRowScale;
+                                           [&](int r, uint32_t top) {
+                                             S.row_scale[r] = fabsf(scale) * query_row_down(top) * kLog2e * kRowScale;
                                            });
       fence_proxy_async_smem();
       named_bar_sync(kBarSoft, kGSoftWarps * 32);

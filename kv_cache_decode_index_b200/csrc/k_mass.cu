@@ -11,14 +11,19 @@
 //     into a ring of two 32 KB pairs of slots.  Entries are 288 bytes each where
 //     a query row is 1 KB, so this is the side to stream; for single tokens it
 //     is the only one that is long.
+//   * The rows' log-sum-exp is taken off by the product itself: one more step of
+//     K holds ones for the entries and -lse, in three fp16 parts, for the rows.  It
+//     comes last, where the sum is small.  So the epilogue needs nothing per
+//     column but a product, exp2 and a sum: factors of each column from shared
+//     memory (which the operands keep busy) had it at 52 cycles a column.
 //   * One warp of the leader issues the MMAs into two 256-column accumulators;
-//     eight warps (lane quarter x half of the columns) take exp2 and the sums.
+//     four warps (a lane quarter each) take exp2 and the sums.
 // Why a pair: shared memory gives 128 bytes a cycle.  One CTA alone would read
 // 128 (operands of M = N = 128) and write 64 (rows); the pair reads 64 and
 // writes 32 for each of its CTAs at the full MMA rate.
 //
 // The work is cut into equal ranges of (row tile, 256 entries) steps, ordered by
-// request, part of 4,096 entries, row tile, tile of entries: a pair holds a
+// request, part of 8,192 entries, row tile, tile of entries: a pair holds a
 // part's sums in shared memory over all row tiles.  Parts that ranges cut are
 // joined in a fixed order by a second launch.
 #include <cuda_bf16.h>
@@ -30,11 +35,11 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kMEpiWarps = 8, kMDeqWarps = 8, kMMmaWarp = kMEpiWarps + kMDeqWarps;
-constexpr int kMThreads = (kMMmaWarp + 1) * 32;   // 544
+constexpr int kMEpiWarps = 4, kMDeqWarps = 8, kMMmaWarp = kMEpiWarps + kMDeqWarps;
+constexpr int kMThreads = (kMMmaWarp + 1) * 32;   // 416
 constexpr int kMKeys = 256;                       // entries of a tile (both CTAs)
 constexpr int kMRows = 256;                       // query rows of a tile (both CTAs)
-constexpr int kMPart = 16;                        // tiles of entries whose sums a pair holds
+constexpr int kMPart = 32;                        // tiles of entries whose sums a pair holds
 constexpr int kMRing = 2;
 constexpr int kMSlot = 128 * 128;                 // 128 rows x 64 channels
 constexpr int kMAcc = 2;
@@ -42,25 +47,41 @@ constexpr uint32_t kMTmemCols = kMAcc * kMRows;   // 512
 constexpr int kMaxPairs = 128;
 constexpr int kBarEpi = 1;
 
+// Queries are scaled by 2^6 in fp16 while every magnitude of a row tile is below
+// 2^9 and every log-sum-exp fits; other tiles ("wide") scale each row by itself
+// and take factors and log-sum-exp per column.
+constexpr int kMExponent = 8;
+constexpr float kMUndo = kRowScale / 64.0f;       // of 2^6 and of the entries' 2^-8
+constexpr float kMLargest = 60000.0f;
+
 struct __align__(1024) MassSmem {
   uint8_t q[kKvDim / 64][kMSlot];                 // B: this CTA's half of the rows
-  uint8_t ring[kMRing][2 * kMSlot];               // A: 128 entries, 128 channels a pair
+  union {
+    uint8_t ring[kMRing][2 * kMSlot];             // A: 128 entries, 128 channels a pair
+    struct {                                      // plan, before the first pair is filled
+      int ctx[kMaxDenseBatch];
+      long long at[kMaxDenseBatch + 1];           // steps before each request
+    };
+  };
+  uint8_t a_ones[128 * 32];                       // the last step of K: A ...
+  uint8_t b_lse[128 * 32];                        // ... and B
   float col_scale[2][kMRows];                     // per column: factor of the scores (by turns: the
                                                   // other CTA fills its half of the next one) ...
   float col_lse2[kMRows];                         // ... log2 of the row's sum ...
   int col_lim[kMRows];                            // ... and entries that it sees (0: no row)
-  float sum[2][kMPart * kMKeys / 2];              // this CTA's entries of the part, per half of the columns
+  float sum[kMPart * kMKeys / 2];                 // this CTA's entries of the part
   int warp_min[kMEpiWarps];
-  int ctx[kMaxDenseBatch];
-  long long at[kMaxDenseBatch + 1];               // steps before each request
+  float wide[2];                                  // by turns: some row of either CTA needs the wide form
   uint64_t full[kMRing];                          // leader: both CTAs' dequantisation
   uint64_t empty[kMRing];
   uint64_t acc_full[kMAcc];
   uint64_t acc_empty[kMAcc];                      // leader
   uint64_t q_full;                                // leader
-  uint64_t scale_full;                            // the other CTA's rows' factors have arrived
+  uint64_t scale_full;                            // what the other CTA says of its rows has arrived
   uint64_t drain;
   uint32_t tmem_base;
+  int start_b;                                    // the request of the first step, and the steps before it
+  long long start_at;
 };
 static_assert(sizeof(MassSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
@@ -121,6 +142,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
     mbar_init(&S.q_full, 2 * kMEpiWarps);
     mbar_init(&S.scale_full, kMEpiWarps);
     mbar_init(&S.drain, 1);
+    S.wide[0] = S.wide[1] = 0.0f;
     fence_barrier_init();
   }
   __syncthreads();
@@ -150,17 +172,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   const int used = static_cast<int>(min(total, static_cast<long long>(pairs)));
   const long long lo = pair < used ? total * pair / used : total;
   const long long hi = pair < used ? total * (pair + 1) / used : total;
+  if (warp == 0 && lo < hi) {                     // the last request that starts at or before lo
+    int at_b = 0;
+    for (int b = lane; b < cache.batch; b += 32)
+      if (S.at[b] <= lo && S.at[b + 1] > lo) at_b = b;
+    at_b = __reduce_max_sync(0xffffffffu, at_b);
+    if (lane == 0) S.start_b = at_b, S.start_at = S.at[at_b];
+  }
+  // the constant operand of the last step of K: ones in three of its 16 channels
+  for (int i = tid; i < 128 * 8; i += kMThreads) {
+    const int row = i >> 3, word = i & 7;
+    const uint32_t v = word == 0 ? 0x3C003C00u : (word == 1 ? 0x00003C00u : 0u);
+    *reinterpret_cast<uint32_t*>(S.a_ones + sw32_offset(row, word * 4)) = v;
+  }
+  fence_proxy_async_smem();
+  __syncthreads();             // the plan's tables are read; the ring may be filled
 
-  // The run at step pos (b: a request not behind it).
-  auto run_at = [&](long long pos, int b) {
+  // Steps of request b, and the run at step pos (place: a request not behind
+  // it and the steps before that one).
+  struct Walk {
+    int b;
+    long long at;
+  };
+  auto steps_of = [&](int b) {
+    const int n = queries_of(a, b, kKMass, false);
+    const int ctx = n > 0 ? max(0, checked_ctx_len(cache, b, capacity, kKMass, false)) : 0;
+    return static_cast<long long>((ctx + kMKeys - 1) / kMKeys) * ((static_cast<long long>(n) * a.heads + kMRows - 1) / kMRows);
+  };
+  auto run_at = [&](long long pos, Walk& w) {
     Run u;
-    while (S.at[b + 1] <= pos) ++b;
+    for (long long n = steps_of(w.b); w.at + n <= pos; n = steps_of(w.b)) w.at += n, ++w.b;
+    const int b = w.b;
     u.b = b;
-    u.ctx = S.ctx[b];
+    u.ctx = cache.ctx_len[b];
     u.q0 = a.q_start ? a.q_start[b] : b;
     u.rows = (a.q_start ? a.q_start[b + 1] - u.q0 : 1) * a.heads;
     const int row_tiles = (u.rows + kMRows - 1) / kMRows, key_tiles = (u.ctx + kMKeys - 1) / kMKeys;
-    const long long r = pos - S.at[b], per = static_cast<long long>(kMPart) * row_tiles;
+    const long long r = pos - w.at, per = static_cast<long long>(kMPart) * row_tiles;
     u.part = static_cast<int>(r / per) * kMPart;
     const int tiles = min(kMPart, key_tiles - u.part);
     const long long in = r % per;
@@ -185,7 +233,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   if (tid == 0 && rank == 0) {
     MassRecord r = {lo, lo, lo, 0, 0, used, 0};
     if (lo < hi) {
-      const Run u = run_at(lo, 0);
+      Walk w = {S.start_b, S.start_at};
+      const Run u = run_at(lo, w);
       r.part_lo = u.part_lo;
       r.part_hi = u.part_hi;
       r.b = u.b;
@@ -198,52 +247,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   if (warp < kMEpiWarps) {
     // ================= query rows, exp2 and the sums =================
     const uint32_t q_full = map_rank(smem_u32(&S.q_full), 0);
-    const int quarter = warp & 3, hc = warp >> 2, slot = quarter * 32 + lane;   // entry of this CTA's 128, half of the columns
-    const uint32_t tm_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tm_lane = tmem + (static_cast<uint32_t>(warp * 32) << 16);   // thread: entry tid of this CTA's 128
     const float sign = scale < 0.0f ? -1.0f : 1.0f;
-    int item = 0, b = 0, held_b = -1, held_rt = -1, loads = 0, min_lim = 0;
-    // 16 columns of an entry.  Their factors are loaded in one go before the
-    // scores are awaited; the masked form stands apart, so that no branch lies
-    // between two columns.
-    struct Columns {
-      float4 f[4], l[4];
-    };
-    auto factors = [&](int c, Columns& x) {
-      const uint32_t fs = smem_u32(&S.col_scale[loads & 1][c]), ls = smem_u32(&S.col_lse2[c]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x.f[j] = ld_shared_f4(fs + j * 16);
-        x.l[j] = ld_shared_f4(ls + j * 16);
-      }
-    };
-    auto add_weights = [&](const uint32_t (&r)[16], const Columns& x, int c, int key, bool mask, float (&part)[4]) {
+    int item = 0, held_b = -1, held_rt = -1, loads = 0, told = 0, min_lim = 0;
+    Walk walk = {S.start_b, S.start_at};
+    bool wide = false;
+    const float c2 = fabsf(scale) * kLog2e * kMUndo;        // log2 units of an accumulator's unit
+    // 16 of the 32 columns of an entry in r (from `o` on)
+    auto add_fast = [&](const uint32_t (&r)[32], int o, int c, int key, bool mask, float (&part)[4]) {
       if (!mask) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          part[0] += ex2(fmaf(__uint_as_float(r[4 * j]), x.f[j].x, -x.l[j].x));
-          part[1] += ex2(fmaf(__uint_as_float(r[4 * j + 1]), x.f[j].y, -x.l[j].y));
-          part[2] += ex2(fmaf(__uint_as_float(r[4 * j + 2]), x.f[j].z, -x.l[j].z));
-          part[3] += ex2(fmaf(__uint_as_float(r[4 * j + 3]), x.f[j].w, -x.l[j].w));
-        }
+        for (int j = 0; j < 16; ++j) part[j & 3] += ex2(__uint_as_float(r[o + j]) * c2);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int4 lim = *reinterpret_cast<const int4*>(S.col_lim + c + 4 * j);
-          part[0] += key < lim.x ? ex2(fmaf(__uint_as_float(r[4 * j]), x.f[j].x, -x.l[j].x)) : 0.0f;
-          part[1] += key < lim.y ? ex2(fmaf(__uint_as_float(r[4 * j + 1]), x.f[j].y, -x.l[j].y)) : 0.0f;
-          part[2] += key < lim.z ? ex2(fmaf(__uint_as_float(r[4 * j + 2]), x.f[j].z, -x.l[j].z)) : 0.0f;
-          part[3] += key < lim.w ? ex2(fmaf(__uint_as_float(r[4 * j + 3]), x.f[j].w, -x.l[j].w)) : 0.0f;
+          part[0] += key < lim.x ? ex2(__uint_as_float(r[o + 4 * j]) * c2) : 0.0f;
+          part[1] += key < lim.y ? ex2(__uint_as_float(r[o + 4 * j + 1]) * c2) : 0.0f;
+          part[2] += key < lim.z ? ex2(__uint_as_float(r[o + 4 * j + 2]) * c2) : 0.0f;
+          part[3] += key < lim.w ? ex2(__uint_as_float(r[o + 4 * j + 3]) * c2) : 0.0f;
         }
       }
     };
+    // the wide form: each column's factor and log2 of its sum
+    auto add_wide = [&](const uint32_t (&r)[32], int o, int c, int key, float (&part)[4]) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float p = ex2(fmaf(__uint_as_float(r[o + j]), S.col_scale[loads & 1][c + j], -S.col_lse2[c + j]));
+        part[j & 3] += key < S.col_lim[c + j] ? p : 0.0f;
+      }
+    };
+    // Tells the other CTA (its warps wait for all of this CTA's) and hears from it.
+    auto exchange = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(&S.scale_full), rank ^ 1u));
+      ok = mbar_wait_cluster_all(&S.scale_full, told & 1, wait_ns) && ok;
+      ++told;
+    };
     bool fresh = true;                              // no part is held
     for (long long pos = lo; ok && pos < hi;) {
-      const Run u = run_at(pos, b);
-      b = u.b;
+      const Run u = run_at(pos, walk);
       pos += u.kt1 - u.kt0;
       const int end = seen_end(u), N = columns(u), half = N / 2;
       if (fresh) {
-        for (int kt = 0; kt < kMPart; ++kt) S.sum[hc][kt * (kMKeys / 2) + slot] = 0.0f;
+        for (int kt = 0; kt < kMPart; ++kt) S.sum[kt * (kMKeys / 2) + tid] = 0.0f;
         fresh = false;
       }
       if (u.kt0 < end) {
@@ -255,41 +302,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           held_rt = u.rt;
           const int in_tile = min(kMRows, u.rows - u.rt * kMRows);
           const long long row0 = static_cast<long long>(u.q0) * a.heads + u.rt * kMRows;
-          // this CTA's half of the rows; the column tables hold both halves
           ++loads;
-          float* table = S.col_scale[loads & 1] + rank * half;
-          const uint32_t there = map_rank(smem_u32(table), rank ^ 1u);
-          load_query_rows<128, kMEpiWarps>(q, row0 + static_cast<int>(rank) * half, in_tile - static_cast<int>(rank) * half,
-                                           half, sign, S.q[0], warp, lane, [&](int r, float down) {
-                                             const float f = down * fabsf(scale) * kLog2e * kRowScale;
-                                             table[r] = f;
-                                             st_cluster(there + r * 4, f);
-                                           });
-          if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(&S.scale_full), rank ^ 1u));
+          const int turn = loads & 1;
+          if (tid == 0) S.wide[turn ^ 1] = 0.0f;        // (the other CTA writes it after it has heard of this turn)
+          // this CTA's half of the rows; the column tables hold both halves
+          bool large = !(c2 > 0.01f);
+          const int mine = in_tile - static_cast<int>(rank) * half;
+          load_query_rows<128, kMEpiWarps, kMExponent>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0],
+                                                       warp, lane, [&](int, uint32_t top) {
+                                                         large = large || top >= (127u + kMExponent + 1) << 7;
+                                                       });
           int lowest = 0x7FFFFFFF;
           for (int c = tid; c < N; c += kMEpiWarps * 32) {
             int lim = 0;
-            float l2 = 0.0f;
+            float l = 0.0f;
             if (c < in_tile) {
               lim = seen_by(a.q_pos[u.q0 + (u.rt * kMRows + c) / a.heads], a.ratio, u.ctx);
-              l2 = lse[row0 + c] * kLog2e;
+              l = lse[row0 + c];
+              lowest = min(lowest, lim);
             }
             S.col_lim[c] = lim;
-            S.col_lse2[c] = l2;
-            lowest = min(lowest, lim);
+            S.col_lse2[c] = l * kLog2e;
+            // -lse in the accumulator's unit: three fp16 parts hold an fp32 value
+            // whole (columns without a row: far below everything)
+            float v = c < in_tile ? (lim > 0 ? -l * (kLog2e / c2) : 0.0f) : -kMLargest;
+            if (!(fabsf(v) <= kMLargest)) large = true, v = 0.0f;
+            const int r = c - static_cast<int>(rank) * half;
+            if (r >= 0 && r < half) {
+              const __half h0 = __float2half_rn(v), h1 = __float2half_rn(v - __half2float(h0));
+              const __half h2 = __float2half_rn(v - __half2float(h0) - __half2float(h1));
+              const uint32_t w0 = __half_as_ushort(h0) | (static_cast<uint32_t>(__half_as_ushort(h1)) << 16);
+              *reinterpret_cast<uint4*>(S.b_lse + sw32_offset(r, 0)) = make_uint4(w0, __half_as_ushort(h2), 0u, 0u);
+              *reinterpret_cast<uint4*>(S.b_lse + sw32_offset(r, 16)) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
-          min_lim = __reduce_min_sync(0xffffffffu, lowest);
-          if (lane == 0) S.warp_min[warp] = min_lim;
+          lowest = __reduce_min_sync(0xffffffffu, lowest);
+          if (lane == 0) S.warp_min[warp] = lowest;
+          if (__any_sync(0xffffffffu, large) && lane == 0) {
+            S.wide[turn] = 1.0f;
+            st_cluster(map_rank(smem_u32(&S.wide[turn]), rank ^ 1u), 1.0f);
+          }
           fence_proxy_async_smem();
           named_bar_sync(kBarEpi, kMEpiWarps * 32);
           min_lim = __reduce_min_sync(0xffffffffu, S.warp_min[lane % kMEpiWarps]);
+          exchange();
+          wide = *reinterpret_cast<volatile float*>(&S.wide[turn]) != 0.0f;
+          if (wide) {
+            // Columns' factors, of both CTAs' rows, and rows scaled by themselves
+            float* table = S.col_scale[turn] + rank * half;
+            const uint32_t there = map_rank(smem_u32(table), rank ^ 1u);
+            load_query_rows<128, kMEpiWarps, kPerRow>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0], warp,
+                                                      lane, [&](int r, uint32_t top) {
+                                                        const float f = query_row_down(top) * fabsf(scale) * kLog2e * kRowScale;
+                                                        table[r] = f;
+                                                        st_cluster(there + r * 4, f);
+                                                      });
+            for (int i = tid; i < 128 * 2; i += kMEpiWarps * 32)
+              reinterpret_cast<uint4*>(S.b_lse)[i] = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            named_bar_sync(kBarEpi, kMEpiWarps * 32);
+            exchange();
+          }
           if (lane == 0) mbar_arrive_cluster(q_full);
-          ok = mbar_wait_cluster_all(&S.scale_full, (loads - 1) & 1, wait_ns);
         }
       }
       for (int kt = u.kt0; ok && kt < end; ++kt, ++item) {
         const int k0 = (u.part + kt) * kMKeys, key0 = k0 + static_cast<int>(rank) * (kMKeys / 2);
-        const int key = key0 + slot;
+        const int key = key0 + tid;
         int page = -1;                               // of this CTA's entries
         if (key0 < u.ctx) page = cache.page_table[static_cast<long long>(u.b) * cache.max_pages_per_req + key0 / cache.page_size];
         const bool mask = min_lim < min(k0 + kMKeys, u.ctx);
@@ -299,42 +378,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
         if (!ok) break;
         tc_fence_after();
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint32_t r0[16], r1[16];                     // tensor-memory loads run one part ahead
-        Columns x;
-        const int cb = hc * half, ce = cb + half;    // this warp's columns (a multiple of 16)
+        // Tensor-memory loads of 32 columns run one ahead: each takes about 500
+        // cycles next to the MMAs (with 16 the wait for them was most of the time).
+        uint32_t r0[32], r1[32];
         const uint32_t from = tm_lane + acc * kMRows;
-        tmem_ld_32x32b_x16(from + cb, r0);
+        auto add = [&](const uint32_t (&r)[32], int c) {
+#pragma unroll
+          for (int o = 0; o < 32; o += 16) {
+            if (wide) add_wide(r, o, c + o, key, part);
+            else add_fast(r, o, c + o, key, mask, part);
+          }
+        };
+        tmem_ld_32x32b_x32(from, r0);
 #pragma unroll 1
-        for (int c = cb; c < ce; c += 32) {
-          factors(c, x);
+        for (int c = 0; c < N; c += 64) {            // (N is a multiple of 32)
           tmem_ld_wait();
-          if (c + 16 < ce) tmem_ld_32x32b_x16(from + c + 16, r1);
-          add_weights(r0, x, c, key, mask, part);
-          if (c + 16 < ce) {
-            factors(c + 16, x);
+          if (c + 32 < N) tmem_ld_32x32b_x32(from + c + 32, r1);
+          add(r0, c);
+          if (c + 32 < N) {
             tmem_ld_wait();
-            if (c + 32 < ce) tmem_ld_32x32b_x16(from + c + 32, r0);
-            add_weights(r1, x, c + 16, key, mask, part);
+            if (c + 64 < N) tmem_ld_32x32b_x32(from + c + 64, r0);
+            add(r1, c + 32);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acc_empty[acc]), 0));
-        if (page >= 0 && page < cache.num_pages) S.sum[hc][kt * (kMKeys / 2) + slot] += (part[0] + part[1]) + (part[2] + part[3]);
+        if (page >= 0 && page < cache.num_pages) S.sum[kt * (kMKeys / 2) + tid] += (part[0] + part[1]) + (part[2] + part[3]);
       }
       // the part's end, or the range's: the entries' weights, or this pair's share of them
       if (ok && (pos >= hi || pos >= u.part_hi)) {
         const bool whole = u.part_lo >= lo && u.part_hi <= hi;
         float* share = wsp.part + (2 * static_cast<size_t>(pair) + (u.part_lo < lo ? 0 : 1)) * (kMPart * kMKeys);
-        named_bar_sync(kBarEpi, kMEpiWarps * 32);       // both halves of the columns
 #pragma unroll 4
-        for (int kt = hc; kt < kMPart; kt += 2) {
-          const int in = kt * kMKeys + static_cast<int>(rank) * (kMKeys / 2) + slot, key = u.part * kMKeys + in;
-          const float s = S.sum[0][kt * (kMKeys / 2) + slot] + S.sum[1][kt * (kMKeys / 2) + slot];
+        for (int kt = 0; kt < kMPart; ++kt) {
+          const int in = kt * kMKeys + static_cast<int>(rank) * (kMKeys / 2) + tid, key = u.part * kMKeys + in;
+          const float s = S.sum[kt * (kMKeys / 2) + tid];
           if (!whole) share[in] = s;
           else if (key < u.ctx && s != 0.0f) mass[u.b * capacity + key] += s;
         }
-        named_bar_sync(kBarEpi, kMEpiWarps * 32);
         fresh = true;
       }
     }
@@ -356,14 +438,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
     struct Place {
       int b, key, page, off;
     };
-    auto fetch = [&](const Run& u, int kt) {
+    auto fetch = [&](int b, int ctx, int tile) {
       Place x;
-      x.b = u.b;
-      x.key = (u.part + kt) * kMKeys + static_cast<int>(rank) * (kMKeys / 2);
+      x.b = b;
+      x.key = tile * kMKeys + static_cast<int>(rank) * (kMKeys / 2);
       const int slot = x.key / cache.page_size;
       x.off = x.key - slot * cache.page_size;
       x.page = -2;
-      if (x.key < u.ctx) x.page = cache.page_table[static_cast<long long>(u.b) * cache.max_pages_per_req + slot];
+      if (x.key < ctx) x.page = cache.page_table[static_cast<long long>(b) * cache.max_pages_per_req + slot];
       return x;
     };
     auto row_of_page = [&](const Place& x) {
@@ -384,31 +466,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       sc[i] = *reinterpret_cast<const uint16_t*>(sp + (i >> 2) * 16 + (i & 3) * 32 * kKvScaleBytes);
     };
     // The tiles in order: run by run, the visible ones.
-    int b = 0;
+    Walk walk = {S.start_b, S.start_at};
     long long pos = lo;
-    Run u = {};
-    int kt = 0, end = 0;
+    int tb = 0, tctx = 0, tile = 0, left = 0;        // the tile, its request, and the tiles left of its run
     auto next_tile_of = [&]() {                      // advances to a tile; false at the range's end
-      ++kt;
-      while (kt >= end) {
+      ++tile;
+      --left;
+      while (left <= 0) {
         if (pos >= hi) return false;
-        u = run_at(pos, b);
-        b = u.b;
+        const Run u = run_at(pos, walk);
         pos += u.kt1 - u.kt0;
-        kt = u.kt0;
-        end = seen_end(u);
+        tb = u.b;
+        tctx = u.ctx;
+        tile = u.part + u.kt0;
+        left = seen_end(u) - u.kt0;
       }
       return true;
     };
     bool have = next_tile_of(), more = false;        // a tile is loaded; another one comes after it
     Place ahead = {};
     if (have) {
-      aim(row_of_page(fetch(u, kt)));
+      aim(row_of_page(fetch(tb, tctx, tile)));
 #pragma unroll
       for (int i = 0; i < 8; ++i) load(i);
       mask = next_mask;
       more = next_tile_of();
-      if (more) ahead = fetch(u, kt);
+      if (more) ahead = fetch(tb, tctx, tile);
     }
     int n = grp;                                     // this group's next pair in the order of all pairs
     while (ok && have) {
@@ -416,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       if (more) {
         aim(row_of_page(ahead));
         more = next_tile_of();
-        if (more) ahead = fetch(u, kt);
+        if (more) ahead = fetch(tb, tctx, tile);
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p, n += 2) {
@@ -445,11 +528,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
     // ================= MMA issuer =================
     const bool issue = elect_one();
     const uint64_t k_desc = sw128_kmajor_desc(smem_u32(S.ring[0])), q_desc = sw128_kmajor_desc(smem_u32(S.q[0]));
-    int s = 0, item = 0, loads = 0, b = 0, held_b = -1, held_rt = -1;
+    const uint64_t ones_desc = sw32_kmajor_desc(smem_u32(S.a_ones)), lse_desc = sw32_kmajor_desc(smem_u32(S.b_lse));
+    Walk walk = {S.start_b, S.start_at};
+    int s = 0, item = 0, loads = 0, held_b = -1, held_rt = -1;
     uint32_t phase = 0;
     for (long long pos = lo; ok && pos < hi;) {
-      const Run u = run_at(pos, b);
-      b = u.b;
+      const Run u = run_at(pos, walk);
       pos += u.kt1 - u.kt0;
       const int end = seen_end(u);
       if (u.kt0 >= end) continue;
@@ -476,7 +560,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
               umma_f16_pair(tmem + acc * kMRows, ad + (kk >> 2) * (kMSlot / 16) + (kk & 3) * 2,
                             bd + (kk >> 2) * (kMSlot / 16) + (kk & 3) * 2, idesc, (c | kk) > 0 ? 1u : 0u);
             umma_commit_pair(&S.empty[s]);
-            if (c == 3) umma_commit_pair(&S.acc_full[acc]);
+            if (c == 3) {
+              umma_f16_pair(tmem + acc * kMRows, ones_desc, lse_desc, idesc, 1u);
+              umma_commit_pair(&S.acc_full[acc]);
+            }
           }
           __syncwarp();
           if (++s == kMRing) {

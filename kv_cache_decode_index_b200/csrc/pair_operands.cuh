@@ -50,12 +50,14 @@ __device__ __forceinline__ float query_row_down(uint32_t top) { return exp2i(que
 // Query rows first .. first + kRows - 1 of q (bf16 [..][512]) as a K-major
 // operand in 64-channel parts of kRows rows at `dst`: fp16 with a power-of-two
 // scale per row (bf16's 8 bits are kept whole; the row's largest value comes to
-// lie in [2^14, 2^15)), eight rows' loads in flight per warp.  Rows from `valid`
-// on are zeros; rows from `limit` on are left out.  scale_of(row, down) is called
-// by one lane with the factor that undoes the row's scale.
-template <int kRows, int kWarps, class ScaleOf>
+// lie in [2^14, 2^15)), or 2^(14 - kExponent) for every row, eight rows' loads
+// in flight per warp.  Rows from `valid` on are zeros; rows from `limit` on are
+// left out.  seen(row, top) is called by one lane with the bits of the row's
+// largest magnitude.
+constexpr int kPerRow = 1000;
+template <int kRows, int kWarps, int kExponent, class Seen>
 __device__ __forceinline__ void load_query_rows(const __nv_bfloat16* __restrict__ q, long long first, int valid, int limit,
-                                                float sign, uint8_t* dst, int warp, int lane, ScaleOf scale_of) {
+                                                float sign, uint8_t* dst, int warp, int lane, Seen seen) {
 #pragma unroll 1
   for (int r0 = warp; r0 < limit; r0 += 8 * kWarps) {
     uint4 v[8][2];
@@ -78,7 +80,7 @@ __device__ __forceinline__ void load_query_rows(const __nv_bfloat16* __restrict_
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = max(top, max(wv[k] & 0x7FFFu, (wv[k] >> 16) & 0x7FFFu));
       top = __reduce_max_sync(0xffffffffu, top);
-      const float up = exp2i(14 - query_row_exponent(top)) * sign;
+      const float up = exp2i(14 - (kExponent == kPerRow ? query_row_exponent(top) : kExponent)) * sign;
       uint32_t hv[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -88,7 +90,7 @@ __device__ __forceinline__ void load_query_rows(const __nv_bfloat16* __restrict_
       const int c0 = 2 * (lane & 3);
       *reinterpret_cast<uint4*>(at + ((c0 ^ (r & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
       *reinterpret_cast<uint4*>(at + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-      if (lane == 0) scale_of(r, query_row_down(top));
+      if (lane == 0) seen(r, top);
     }
   }
 }

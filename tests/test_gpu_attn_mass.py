@@ -130,6 +130,68 @@ def test_attn_mass_recorded_violations(csa2):  # noqa: F811
         _check(mass[1:], torch.zeros_like(mass[1:]), want[1:], tol[1:], lens[1:])
 
 
+@pytest.mark.parametrize("what", ["large", "tiny", "lse", "scale"])
+def test_attn_mass_wide_rows(csa2, what):  # noqa: F811
+    """Row tiles that leave the common scale: very large or very small queries,
+    log-sum-exps far from the scores, a small scale; an ordinary tile and
+    request next to them."""
+    lens, new, H = [300, 200], [40, 7], 16
+    case = _case(csa2, lens, new, H, 128, seed=8)
+    cache, table, codes, scales, start, pos, q = case
+    scale = 1 / math.sqrt(512)
+    if what == "large":
+        q[5, 3] *= 2.0 ** 13                      # scores of thousands: one entry takes all
+        q[38] *= 2.0 ** 30
+    elif what == "tiny":
+        q[5] *= 2.0 ** -40
+        q[30] = 0
+    elif what == "scale":
+        scale = 1e-4
+    if what == "large":
+        # Rows (5, 3) and 38 have scores up to 10^4 and 10^10.  fp32 holds such an
+        # lse to 2^-8 and to 2^9 only, so exp(score - lse) of their largest
+        # entries may be off by any factor up to e^(2^9): nothing is asked of the
+        # entries whose score lies within the scores' own error d, that spacing
+        # and 110 (e^-110 is below fp32) of the largest.  Every other entry gets
+        # nothing of these rows, and what the other rows give it.
+        lse = torch.empty(q.shape[:2], device="cuda")
+        csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda(), lse=lse, scale=scale)
+        mass = csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, torch.zeros(2, cache.capacity, device="cuda"),
+                              torch.from_numpy(start).cuda(), scale=scale)
+        got = mass.double().cpu().numpy()
+        for b, (a, z) in enumerate(((0, 40), (40, 47))):
+            K = O.keys(table, 128, codes, scales, b, lens[b])
+            seen = pos[a:z] + 1
+            q64 = q[a:z].double().cpu().numpy()
+            s = np.where(np.arange(lens[b])[None, None] < seen[:, None, None], np.einsum("ihc,ec->ihe", q64, K) * scale, -np.inf)
+            size = scale * np.einsum("ihc,ec->ihe", np.abs(q64), np.abs(K)).max(-1)
+            l = lse[a:z].double().cpu().numpy()
+            d = (512 + 4) * 2.0 ** -23 * size + 2.0 ** -22 + 2.0 ** -23 * np.abs(l)
+            d = 2 * d                               # the scores here, and those that the lse was made of
+            far = d >= 1.0
+            assert far.sum() == (17 if b == 0 else 0)
+            near = (far[..., None] & (s >= s.max(-1, keepdims=True) - (110 + 2 * d + 2.0 ** 10)[..., None])).any((0, 1))
+            p = np.where(np.isfinite(s) & ~far[..., None], np.exp(np.where(np.isfinite(s), s - l[..., None], 0.0) * ~far[..., None]), 0.0)
+            want, tol = p.sum((0, 1)), (p * 2 * np.minimum(d, 1.0)[..., None]).sum((0, 1)) + 700 * 2.0 ** -24 * p.sum((0, 1))
+            err = np.abs(got[b, :lens[b]] - want)[~near]
+            assert (~near).any() and (err <= tol[~near]).all(), (b, err.max())
+        return
+    lse, want, tol = _reference(case, lens, 1, scale)
+    if what == "lse":                             # as if most of the weight lay elsewhere
+        lse[4] += 3.0e4
+        lse[20] += 5.0
+    mass = torch.zeros(2, cache.capacity, device="cuda")
+    csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(start).cuda(), scale=scale)
+    if what == "lse":
+        K = O.keys(table, 128, codes, scales, 0, 300)
+        ref = O.attention(q[:40].double().cpu().numpy(), K, pos[:40] + 1, scale)
+        l = lse[:40].double().cpu().numpy()
+        p = np.where(np.isfinite(ref["s"]), np.exp(np.where(np.isfinite(ref["s"]), ref["s"] - l[..., None], 0.0)), 0.0)
+        d = (512 + 4) * 2.0 ** -23 * ref["size"] + 2.0 ** -22 + 2.0 ** -23 * np.abs(l)
+        want[0], tol[0] = p.sum((0, 1)), (p * 2 * d[..., None]).sum((0, 1)) + (40 * H + 4) * 2.0 ** -24 * p.sum((0, 1))
+    _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
 def test_attn_mass_graph(csa2):  # noqa: F811
     lens, new, H = [700, 90], [33, 20], 32
     case = _case(csa2, lens, new, H, 128, seed=15)

@@ -1,6 +1,6 @@
-// Work plan of the dense operators (csa2_chunk_attn, csa2_attn_mass): query
+// Work plan of csa2_chunk_attn (and what csa2_attn_mass shares of it): query
 // tiles of one request each, a tile's keys in steps, and the whole list of
-// (tile, step) pairs cut into equal ranges, one per CTA.
+// (tile, step) pairs cut into equal ranges, one per CTA (or pair of CTAs).
 //
 // Lengths live on the device, so every CTA derives the same plan from them at
 // its start: tiles per request, steps per tile (the keys that the tile's most
@@ -22,7 +22,6 @@ struct DenseArgs {
   int ratio;                // tokens per entry
   int heads;
   int tile_tokens;          // tokens per query tile
-  int min_steps;            // a range is at least this long
 };
 
 constexpr int kMaxDenseBatch = 1024;
@@ -106,6 +105,24 @@ __device__ __forceinline__ int dense_steps(const DenseTile& t) {
   return max(1, (t.keys + kStep - 1) / kStep);   // a tile that sees nothing still writes its rows
 }
 
+// Starting and ending a tile costs about as much as two of its steps, so the
+// plan counts kTileCost steps more for each, before its own: with none a range
+// of many short tiles took twice as long as the others.
+constexpr int kTileCost = 2;
+// The part [first, first + n) of a tile's own steps that lies in a range which
+// starts `off` counted steps into the tile and has `left` left; n may be 0.
+struct TilePart {
+  int counted;                           // of the range's steps
+  int first, n;
+};
+__device__ __forceinline__ TilePart tile_part(int steps, int off, long long left) {
+  TilePart t;
+  t.counted = static_cast<int>(min(static_cast<long long>(steps + kTileCost - off), left));
+  t.first = max(0, off - kTileCost);
+  t.n = max(0, off + t.counted - kTileCost - t.first);
+  return t;
+}
+
 // Every thread of the block calls this.
 template <int kThreads, int kStep>
 __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSmem<kThreads>& S, int cta, int ctas,
@@ -150,7 +167,7 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
   };
   auto steps_of = [&](TilePlace at) {
     const int n = a.q_start ? a.q_start[at.b + 1] - a.q_start[at.b] : 1;
-    return dense_steps<kStep>(dense_tile(a, at, n, S.ctx[at.b]));
+    return dense_steps<kStep>(dense_tile(a, at, n, S.ctx[at.b])) + kTileCost;
   };
   long long mine = 0;
   for (int t = t0; t < t1; ++t) mine += steps_of(place_of(t));
@@ -167,8 +184,7 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
     if (w < warp) before += S.warp_sum[w];
     total += S.warp_sum[w];
   }
-  const long long most = (total + a.min_steps - 1) / a.min_steps;
-  p.ctas = static_cast<int>(most < ctas ? most : ctas);
+  p.ctas = static_cast<int>(total < ctas ? total : ctas);
   if (cta < p.ctas) {
     p.lo = total * cta / p.ctas;
     p.hi = total * (cta + 1) / p.ctas;
@@ -193,15 +209,5 @@ __device__ __forceinline__ DensePlan dense_plan(const DenseArgs& a, DensePlanSme
   p.off = S.off;
   return p;
 }
-
-// What a CTA says of its range, for the launch that joins split tiles.
-struct RangeRecord {
-  long long lo;          // first step
-  long long tile_lo;     // first step of the tile that it starts in
-  long long tile_hi;     // behind that tile's last step
-  int q0, tokens;        // that tile's queries
-  int ctas;              // CTAs that have work
-  int pad;
-};
 
 }  // namespace csa2

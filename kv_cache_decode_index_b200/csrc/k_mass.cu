@@ -122,6 +122,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   const MassWorkspace wsp = split_mass_ws(ws);
   const long long capacity = static_cast<long long>(cache.max_pages_per_req) * cache.page_size;
 
+  pdl_launch_dependents();     // the joining launch: it waits for this one's end
+
   // ---- plan: steps of each request = its tiles of entries x its row tiles ----
   for (int b = tid; b < cache.batch; b += kMThreads) {
     const int n = queries_of(a, b, kKMass, blockIdx.x == 0);
@@ -277,11 +279,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
         part[j & 3] += key < S.col_lim[c + j] ? p : 0.0f;
       }
     };
-    // Tells the other CTA (its warps wait for all of this CTA's) and hears from it.
+    // Tells the other CTA (its warps wait for all of this CTA's) and hears from
+    // it; whether one warp's wait ran out is voted on, so that all four leave.
     auto exchange = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(&S.scale_full), rank ^ 1u));
-      ok = mbar_wait_cluster_all(&S.scale_full, told & 1, wait_ns) && ok;
+      ok = mbar_wait_cluster_all(&S.scale_full, told & 1, wait_ns);
+      ok = !named_bar_or(kBarEpi, kMEpiWarps * 32, !ok);
       ++told;
     };
     bool fresh = true;                              // no part is held
@@ -346,6 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           named_bar_sync(kBarEpi, kMEpiWarps * 32);
           min_lim = __reduce_min_sync(0xffffffffu, S.warp_min[lane % kMEpiWarps]);
           exchange();
+          if (!ok) break;
           wide = *reinterpret_cast<volatile float*>(&S.wide[turn]) != 0.0f;
           if (wide) {
             // Columns' factors, of both CTAs' rows, and rows scaled by themselves
@@ -362,6 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
             fence_proxy_async_smem();
             named_bar_sync(kBarEpi, kMEpiWarps * 32);
             exchange();
+            if (!ok) break;
           }
           if (lane == 0) mbar_arrive_cluster(q_full);
         }
@@ -373,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
         if (key0 < u.ctx) page = cache.page_table[static_cast<long long>(u.b) * cache.max_pages_per_req + key0 / cache.page_size];
         const bool mask = min_lim < min(k0 + kMKeys, u.ctx);
         const int acc = item % kMAcc;
-        ok = mbar_wait_warp(&S.acc_full[acc], (item / kMAcc) & 1, wait_ns);
+        ok = mbar_wait_all(&S.acc_full[acc], (item / kMAcc) & 1, wait_ns);
         ok = !named_bar_or(kBarEpi, kMEpiWarps * 32, !ok);
         if (!ok) break;
         tc_fence_after();
@@ -504,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
 #pragma unroll
       for (int p = 0; p < 2; ++p, n += 2) {
         const int x2 = n % kMRing;
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&S.empty[x2], ((n / kMRing) & 1) ^ 1, wait_ns)) != 0;
+        ok = ok && mbar_wait_all(&S.empty[x2], ((n / kMRing) & 1) ^ 1, wait_ns);
         if (!ok) continue;
         uint8_t* dst = S.ring[x2] + ksel * kMSlot + krow * 128;
 #pragma unroll
@@ -576,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
     if (lane == 0 && !ok) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, -1, item);
     __syncwarp();
     if (issue) umma_commit_pair(&S.drain);
-    (void)mbar_wait(&S.drain, 0, kWaitLimitNs);
+    (void)mbar_wait_all(&S.drain, 0, kWaitLimitNs);
   } else {
     if (lane == 0) (void)mbar_wait(&S.drain, 0, 4 * kWaitLimitNs);   // the leader's last arrival here
   }
@@ -590,6 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
 // Joins the parts that ranges cut: block (c, y) takes 256 entries of the part
 // that pair c starts inside, if c is the first to do so.
 __global__ void __launch_bounds__(kMKeys) attn_mass_join_kernel(const csa2_cache cache, float* __restrict__ mass, void* ws) {
+  pdl_wait();
   const MassWorkspace wsp = split_mass_ws(ws);
   const int c = blockIdx.x;
   const MassRecord r = wsp.rec[c];
@@ -618,14 +625,22 @@ cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32
     return cudaFuncSetAttribute(attn_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   });
   if (e != cudaSuccess) return e;
-  const DenseArgs a = {cache, q_start, q_pos, n_queries, ratio, H, 1, 1};
+  const DenseArgs a = {cache, q_start, q_pos, n_queries, ratio, H, 1};
   const int pairs = min(kMaxPairs, num_sms / 2);
   attn_mass_kernel<<<2 * pairs, kMThreads, smem, stream>>>(a, reinterpret_cast<const __nv_bfloat16*>(q), scale, lse, mass,
                                                            ws, wait_ns);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_mass_join_kernel<<<dim3(pairs, kMPart), kMKeys, 0, stream>>>(cache, mass, ws);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pairs, kMPart);
+  cfg.blockDim = dim3(kMKeys);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the ranges before reading
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_mass_join_kernel, cache, mass, ws);
 }
 
 }  // namespace csa2

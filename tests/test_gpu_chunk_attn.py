@@ -219,3 +219,24 @@ def test_chunk_attn_offsets_past_32_bits(csa2):
     c2, s2 = np.zeros((2 * page, 256), np.uint8), np.zeros((2 * page, 32), np.uint8)
     c2[:5000], s2[:5000] = codes, scales
     _check(cache, small, c2, s2, [0, 1], pos, q, out, lse, [5000], 1, 1 / math.sqrt(512))
+
+
+def test_chunk_attn_wait_limit(csa2):  # noqa: F811
+    """A wait that runs out is recorded and the launch ends; the next one is
+    unharmed."""
+    args = _case(csa2, [2000, 300], [70, 3], 32, 128, seed=9)
+    cache, start, pos, q = args[0], args[4], args[5], args[6]
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    csa2.set_wait_limit_ns(0)
+    try:
+        csa2.chunk_attn(cache, q, p, s, out=out, lse=lse)
+        st, _ = csa2.get_error(cache)
+    finally:
+        csa2.set_wait_limit_ns(2_000_000_000)
+    assert st == csa2.ERR_TIMEOUT
+    cache.err_word.zero_()
+    csa2.chunk_attn(cache, q, p, s, out=out, lse=lse)
+    st, word = csa2.get_error(cache)
+    assert st == csa2.OK, word
+    _check(*args, out, lse, [2000, 300], 1, 1 / math.sqrt(512))

@@ -448,9 +448,15 @@ __global__ void __launch_bounds__(128, 6) norm_rope_append_kernel(const __grid_c
       sure = sure && c4 == both >> 16;
     }
   }
-  // squares outside [1e-30, 1e30] or not finite: fp32 may have lost them
+  // squares that fp32 may have lost, large values, and anything that is not
+  // finite (a weight or an angle may be the cause; the maxima above drop a NaN)
+  float size = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) size += ey[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) size += ez[j];
   const bool usual = s <= 1e30f && sk <= 1e30f && (s >= 1e-20f || s == 0.0f) && (sk >= 1e-20f || sk == 0.0f) &&
-                     km_hi <= 1e30f && amax_hi <= 1e30f;
+                     size <= 1e24f;
   if (__all_sync(0xffffffffu, sure && usual)) {
     store_row(a.cache, row, p, lane);
     if (a.ik4_codes != nullptr) store_ik4_codes(a.ik4_codes, a.ik4_scales, row, c4, s4, lane);

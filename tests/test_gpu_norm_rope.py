@@ -190,3 +190,34 @@ def test_norm_rope_append_bad_slots(csa2):
         st, word = csa2.get_error(cache)
         assert st == csa2.ERR_DEVICE_BOUNDS, what
         assert int((cache.kv_codes.sum(1) > 0).sum()) == 1
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("where", ["kv_weight", "ik_weight", "kv", "ik"])
+def test_norm_rope_append_not_finite(csa2, where, bad):
+    """A weight or a value that is not finite (or as large as fp32 goes) is
+    stored as csa2_append_kv stores the formula's fp32 row.  Without rotation
+    every channel is by itself, so the formula needs no care in float64."""
+    B = 2
+    a, _ = _cache(csa2, B, 1, 128)
+    b, _ = _cache(csa2, B, 1, 128)
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((B, 640)).astype(np.float32)
+    w = np.ones(640, np.float32)
+    if where.endswith("weight"):
+        w[37 if where == "kv_weight" else 512 + 37] = bad
+    else:
+        x[1, 37 if where == "kv" else 512 + 37] = bad
+    y = np.empty_like(x)
+    with np.errstate(all="ignore"):
+        for sl in (slice(0, 512), slice(512, 640)):
+            v = x[:, sl].astype(np.float64)
+            inv = 1.0 / np.sqrt((v * v).mean(-1, keepdims=True) + np.float64(np.float32(1e-6)))
+            y[:, sl] = (v * inv * w[sl].astype(np.float64)).astype(np.float32)
+    c = lambda t: torch.from_numpy(np.ascontiguousarray(t)).cuda()  # noqa: E731
+    pos = torch.tensor([3, 100], dtype=torch.int32).cuda()
+    none = csa2.Rope()
+    csa2.norm_rope_append(a, c(x[:, :512]), c(x[:, 512:]), pos, none, none, kv_weight=c(w[:512]), ik_weight=c(w[512:]))
+    csa2.append_kv(b, c(y[:, :512]), c(y[:, 512:]), pos)
+    for name in ("kv_codes", "kv_scales", "ik_codes", "ik_exp"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name

@@ -211,7 +211,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       if (seg == 0) continue;
       const int rows = T.tokens * a.heads;           // of the pair
       const int own = static_cast<int>(rank) * kGRows + row;
-      const int lim = own < rows ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : 0;
+      // (a lane without a row follows the tile's keys: with 0 it would hold its
+      // warp to the masked form at every tile)
+      const bool real = own < rows;
+      const int lim = real ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : T.keys;
       load_query_rows<kGRows, kGSoftWarps, kPerRow>(q, static_cast<long long>(T.q0) * a.heads + static_cast<int>(rank) * kGRows,
                                            rows - static_cast<int>(rank) * kGRows, kGRows, sign, S.q[0], warp, lane,
                                            [&](int r, uint32_t top) {
@@ -231,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const bool masked = __any_sync(0xffffffffu, lim < key0 + 128);
-        const bool seen = __any_sync(0xffffffffu, lim > key0);       // by any row of this warp
+        const bool seen = __any_sync(0xffffffffu, real && lim > key0);   // by any row of this warp
         // tensor-memory loads run one part ahead of the arithmetic
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (seen) {

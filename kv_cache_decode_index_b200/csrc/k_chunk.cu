@@ -668,36 +668,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 // Joins the tiles that ranges cut: block (c, x, y) takes 32 rows and 64
 // channels of the tile that range c starts inside, if c is the first to do so.
 // A lane is a row, a warp 8 channels.
-constexpr int kJoinRows = 32, kJoinChannels = 64;
+constexpr int kJoinRows = 32, kJoinChannels = 64, kJoinWarps = 8;
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     chunk_join_kernel(int heads, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, void* ws) {
+  __shared__ float factor[kMaxPairs][kJoinRows], total[kMaxPairs][kJoinRows], red[kJoinWarps][kJoinRows];
+  static_assert(kMaxPairs <= kJoinWarps * 32, "a thread per range");
   pdl_wait();
   const ChunkWorkspace wsp = split_chunk_ws(ws);
   const int c = blockIdx.x;
   const RangeRecord r = wsp.rec[c];
   if (c >= r.pairs || r.lo <= r.tile_lo || wsp.rec[c - 1].lo > r.tile_lo) return;
-  const int row = blockIdx.z * kJoinRows + (threadIdx.x & 31);
-  const int ch = blockIdx.y * kJoinChannels + (threadIdx.x >> 5) * 8;
-  int last = c;                          // the last range with a part of the tile, 32 records at a look
-  for (bool more = true; more;) {
-    const int k = last + 1 + (threadIdx.x & 31);
-    const uint32_t in = __ballot_sync(0xffffffffu, k < r.pairs && wsp.rec[min(k, r.pairs - 1)].lo < r.tile_hi);
-    last += __popc(in);                  // (the records' starts ascend)
-    more = in == 0xffffffffu;
+  if (static_cast<int>(blockIdx.z) * kJoinRows >= r.tokens * heads) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.z * kJoinRows + lane;
+  const int ch = blockIdx.y * kJoinChannels + warp * 8;
+  // parts of the tile: its head is range c - 1's, which ended (or also began)
+  // with it, then those of the ranges that start before its end (they ascend)
+  const int k = threadIdx.x;
+  const int parts = 1 + __syncthreads_count(k >= c && k < r.pairs && wsp.rec[min(k, r.pairs - 1)].lo < r.tile_hi);
+  auto part_of = [&](int i) { return partial_of(wsp, c - 1 + i, i == 0 ? 1 : 0); };
+  // the rows' maxima and sums: the warps share the parts, so that all of a row's
+  // loads are in flight together
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int i = warp; i < parts; i += kJoinWarps) {
+    const float* part = part_of(i);
+    factor[i][lane] = part[kPartialMax + row];       // (rows that are not there: never used)
+    total[i][lane] = part[kPartialSum + row];
+    m = fmaxf(m, factor[i][lane]);
   }
-  if (row >= r.tokens * heads) return;
-  // the tile's head came from range c - 1, which ended (or also began) with it
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int k = c - 1; k <= last; ++k) M = fmaxf(M, partial_of(wsp, k, k < c ? 1 : 0)[kPartialMax + row]);
-  const float ref = M == -INFINITY ? 0.0f : M;
+  red[warp][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, red[w][lane]);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  for (int i = warp; i < parts; i += kJoinWarps) factor[i][lane] = exp2f(factor[i][lane] - ref);
+  __syncthreads();
   float l = 0.0f, o[8] = {};
 #pragma unroll 8
-  for (int k = c - 1; k <= last; ++k) {
-    const float* part = partial_of(wsp, k, k < c ? 1 : 0);
-    const float f = exp2f(part[kPartialMax + row] - ref);
-    l = fmaf(part[kPartialSum + row], f, l);
+  for (int i = 0; i < parts; ++i) {
+    const float* part = part_of(i);
+    const float f = factor[i][lane];
+    l = fmaf(total[i][lane], f, l);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 v = *reinterpret_cast<const float4*>(part + partial_at(row, ch + 4 * h));
@@ -707,6 +720,7 @@ __global__ void __launch_bounds__(256)
       o[4 * h + 3] = fmaf(v.w, f, o[4 * h + 3]);
     }
   }
+  if (row >= r.tokens * heads) return;
   const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
   const long long orow = static_cast<long long>(r.q0) * heads + row;
   uint32_t pk[4];
@@ -716,7 +730,7 @@ __global__ void __launch_bounds__(256)
     pk[h] = *reinterpret_cast<const uint32_t*>(&b);
   }
   *reinterpret_cast<uint4*>(out + orow * kKvDim + ch) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-  if (lse != nullptr && ch == 0) lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
+  if (lse != nullptr && ch == 0) lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -743,7 +757,7 @@ cudaError_t launch_chunk_attn(const csa2_cache& cache, int n_queries, const int3
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pairs, kKvDim / kJoinChannels, kPairRows / kJoinRows);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits for the ranges before reading

@@ -602,10 +602,16 @@ __global__ void __launch_bounds__(kMKeys) attn_mass_join_kernel(const csa2_cache
   const MassRecord r = wsp.rec[c];
   if (c >= r.pairs || r.lo == r.part_lo || wsp.rec[c - 1].lo > r.part_lo) return;
   const int in = blockIdx.y * kMKeys + threadIdx.x, key = r.k0 + in;
+  // pair c - 1's share comes first, then those of the pairs that start before
+  // the part's end (they ascend)
+  static_assert(kMaxPairs <= kMKeys, "a thread per pair");
+  const int k = threadIdx.x;
+  const int end = c + __syncthreads_count(k >= c && k < r.pairs && wsp.rec[min(k, r.pairs - 1)].lo < r.part_hi);
   if (key >= cache.ctx_len[r.b]) return;
   constexpr size_t kShare = kMPart * kMKeys;
   float sum = wsp.part[(2 * static_cast<size_t>(c - 1) + 1) * kShare + in];
-  for (int k = c; k < r.pairs && wsp.rec[k].lo < r.part_hi; ++k) sum += wsp.part[2 * static_cast<size_t>(k) * kShare + in];
+#pragma unroll 8
+  for (int i = c; i < end; ++i) sum += wsp.part[2 * static_cast<size_t>(i) * kShare + in];
   const long long capacity = static_cast<long long>(cache.max_pages_per_req) * cache.page_size;
   if (sum != 0.0f) mass[r.b * capacity + key] += sum;
 }

@@ -134,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < kMRing; ++i) {
-      mbar_init(&S.full[i], kMDeqWarps);         // four warps of each CTA
+      mbar_init(&S.full[i], 2 * kMDeqWarps);     // the eight warps of each CTA
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < kMAcc; ++i) {
@@ -429,14 +429,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
     if (!ok && lane == 0) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, static_cast<int>(rank), item);
   } else if (warp < kMEpiWarps + kMDeqWarps) {
     // ================= dequantisation =================
-    // Four warps fill a pair of slots; group grp takes pairs grp and grp + 2 of a
-    // tile's four.  A granule is 32 channels of an entry; lane: keys krow + 32 i,
-    // granule kg of slot ksel.  A quarter warp holds 4 entries x 2 neighbouring
+    // All eight warps fill a pair of slots together, so that one pair is filled
+    // while the products take the other (with four warps to a pair a slot's
+    // filling and its products took turns).  A granule is 32 channels of an
+    // entry; lane: keys krow and krow + 64, granule kg of slot ksel of each of
+    // a tile's four pairs.  A quarter warp holds 4 entries x 2 neighbouring
     // granules: its 16-byte stores fall into eight different chunks.
-    const int dw = warp - kMEpiWarps, grp = dw >> 2, wi = dw & 3;
-    const int krow = wi * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), kg = (lane >> 2) & 1, ksel = lane >> 4;
-    const int k_code = (2 * grp + ksel) * 32 + kg * 16, k_sc = (2 * grp + ksel) * 4 + kg * 2;
-    uint4 codes[8];                                  // the lane's granules of the tile in turn
+    const int krow = (warp - kMEpiWarps) * 8 + ((lane >> 3) & 1) * 4 + (lane & 3), kg = (lane >> 2) & 1, ksel = lane >> 4;
+    const int k_code = ksel * 32 + kg * 16, k_sc = ksel * 4 + kg * 2;
+    uint4 codes[8];                                  // the lane's granules of the tile in turn: pair, key
     uint32_t sc[8], mask = 0;
     // The page of this CTA's 128 entries is looked up a tile ahead (fetch);
     // row_of_page, half a tile later, gives their first cache row, or -1: not
@@ -468,8 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       next_mask = base < 0 ? 0u : 0x7F7Fu;
     };
     auto load = [&](int i) {
-      codes[i] = *reinterpret_cast<const uint4*>(cp + (i >> 2) * 128 + (i & 3) * 32 * kKvCodeBytes);
-      sc[i] = *reinterpret_cast<const uint16_t*>(sp + (i >> 2) * 16 + (i & 3) * 32 * kKvScaleBytes);
+      codes[i] = *reinterpret_cast<const uint4*>(cp + (i >> 1) * 64 + (i & 1) * 64 * kKvCodeBytes);
+      sc[i] = *reinterpret_cast<const uint16_t*>(sp + (i >> 1) * 8 + (i & 1) * 64 * kKvScaleBytes);
     };
     // The tiles in order: run by run, the visible ones.
     Walk walk = {S.start_b, S.start_at};
@@ -499,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       more = next_tile_of();
       if (more) ahead = fetch(tb, tctx, tile);
     }
-    int n = grp;                                     // this group's next pair in the order of all pairs
+    int n = 0;                                       // the next pair in the order of all pairs
     while (ok && have) {
       have = more;
       if (more) {
@@ -508,21 +509,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
         if (more) ahead = fetch(tb, tctx, tile);
       }
 #pragma unroll
-      for (int p = 0; p < 2; ++p, n += 2) {
+      for (int p = 0; p < 4; ++p, ++n) {
         const int x2 = n % kMRing;
         ok = ok && mbar_wait_all(&S.empty[x2], ((n / kMRing) & 1) ^ 1, wait_ns);
         if (!ok) continue;
         uint8_t* dst = S.ring[x2] + ksel * kMSlot + krow * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           uint4 o[4];
-          dequant_32(codes[4 * p + i], sc[4 * p + i] & mask, o);
+          dequant_32(codes[2 * p + i], sc[2 * p + i] & mask, o);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(dst + i * 32 * 128 + (((kg * 4 + j) ^ (krow & 7)) << 4)) = o[j];
+            *reinterpret_cast<uint4*>(dst + i * 64 * 128 + (((kg * 4 + j) ^ (krow & 7)) << 4)) = o[j];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load(4 * p + i); // the next tile's (at the end: the last one's again)
+        for (int i = 0; i < 2; ++i) load(2 * p + i); // the next tile's (at the end: the last one's again)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.full[x2]), 0));

@@ -38,14 +38,12 @@ namespace {
 constexpr int kMEpiWarps = 4, kMDeqWarps = 8, kMMmaWarp = kMEpiWarps + kMDeqWarps;
 constexpr int kMThreads = (kMMmaWarp + 1) * 32;   // 416
 constexpr int kMKeys = 256;                       // entries of a tile (both CTAs)
-constexpr int kMRows = 256;                       // query rows of a tile (both CTAs)
 constexpr int kMPart = 32;                        // tiles of entries whose sums a pair holds
-constexpr int kMRing = 2;
 constexpr int kMSlot = 128 * 128;                 // 128 rows x 64 channels
+constexpr int kMStage = 128 * (kKvCodeBytes + kKvScaleBytes);   // 128 packed entries
 constexpr int kMAcc = 2;
-constexpr uint32_t kMTmemCols = kMAcc * kMRows;   // 512
 constexpr int kMaxPairs = 128;
-constexpr int kBarEpi = 1;
+constexpr int kBarEpi = 1, kBarDeq = 2;
 
 // Queries are scaled by 2^6 in fp16 while every magnitude of a row tile is below
 // 2^9 and every log-sum-exp fits; other tiles ("wide") scale each row by itself
@@ -54,8 +52,10 @@ constexpr int kMExponent = 8;
 constexpr float kMUndo = kRowScale / 64.0f;       // of 2^6 and of the entries' 2^-8
 constexpr float kMLargest = 60000.0f;
 
+// kMRows: query rows of a tile (both CTAs); kMRing: pairs of slots of entries.
+template <int kMRows, int kMRing, int kMStages>
 struct __align__(1024) MassSmem {
-  uint8_t q[kKvDim / 64][kMSlot];                 // B: this CTA's half of the rows
+  uint8_t q[kKvDim / 64][kMRows / 2 * 128];       // B: this CTA's half of the rows, 64 channels a part
   union {
     uint8_t ring[kMRing][2 * kMSlot];             // A: 128 entries, 128 channels a pair
     struct {                                      // plan, before the first pair is filled
@@ -65,6 +65,7 @@ struct __align__(1024) MassSmem {
   };
   uint8_t a_ones[128 * 32];                       // the last step of K: A ...
   uint8_t b_lse[128 * 32];                        // ... and B
+  uint8_t stage[kMStages * kMStage + 16];         // packed entries on their way: codes, then scales
   float col_scale[2][kMRows];                     // per column: factor of the scores (by turns: the
                                                   // other CTA fills its half of the next one) ...
   float col_lse2[kMRows];                         // ... log2 of the row's sum ...
@@ -79,11 +80,12 @@ struct __align__(1024) MassSmem {
   uint64_t q_full;                                // leader
   uint64_t scale_full;                            // what the other CTA says of its rows has arrived
   uint64_t drain;
+  uint64_t stage_full[kMStages + 1];
+  int stage_row[kMStages + 1];                    // a stage's cache row, -1: not there, -2: no tile
   uint32_t tmem_base;
   int start_b;                                    // the request of the first step, and the steps before it
   long long start_at;
 };
-static_assert(sizeof(MassSmem) + 1024 <= 227 * 1024, "shared memory of one CTA");
 
 // What a pair says of its range, for the joining launch.
 struct MassRecord {
@@ -110,11 +112,16 @@ struct Run {
   long long part_lo, part_hi;       // steps of the whole part
 };
 
+template <int kMRows, int kMRing, int kMStages>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
     attn_mass_kernel(const DenseArgs a, const __nv_bfloat16* __restrict__ q, float scale, const float* __restrict__ lse,
                      float* __restrict__ mass, void* ws, uint64_t wait_ns) {
   extern __shared__ uint8_t smem_raw[];
-  MassSmem& S = *reinterpret_cast<MassSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using Smem = MassSmem<kMRows, kMRing, kMStages>;
+  static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of one CTA");
+  constexpr uint32_t kMTmemCols = kMAcc * kMRows;
+  constexpr int kMQPart = kMRows / 2 * 128;       // bytes of 64 channels of the rows
+  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -137,6 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       mbar_init(&S.full[i], 2 * kMDeqWarps);     // the eight warps of each CTA
       mbar_init(&S.empty[i], 1);
     }
+    for (int i = 0; i < kMStages; ++i) mbar_init(&S.stage_full[i], 1);
     for (int i = 0; i < kMAcc; ++i) {
       mbar_init(&S.acc_full[i], 1);
       mbar_init(&S.acc_empty[i], 2 * kMEpiWarps);
@@ -312,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           // this CTA's half of the rows; the column tables hold both halves
           bool large = !(c2 > 0.01f);
           const int mine = in_tile - static_cast<int>(rank) * half;
-          load_query_rows<128, kMEpiWarps, kMExponent>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0],
+          load_query_rows<kMRows / 2, kMEpiWarps, kMExponent>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0],
                                                        warp, lane, [&](int, uint32_t top) {
                                                          large = large || top >= (127u + kMExponent + 1) << 7;
                                                        });
@@ -356,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
             // Columns' factors, of both CTAs' rows, and rows scaled by themselves
             float* table = S.col_scale[turn] + rank * half;
             const uint32_t there = map_rank(smem_u32(table), rank ^ 1u);
-            load_query_rows<128, kMEpiWarps, kPerRow>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0], warp,
+            load_query_rows<kMRows / 2, kMEpiWarps, kPerRow>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0], warp,
                                                       lane, [&](int r, uint32_t top) {
                                                         const float f = query_row_down(top) * fabsf(scale) * kLog2e * kRowScale;
                                                         table[r] = f;
@@ -460,7 +468,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       if (x.page != -2) report_error(cache.err_word, CSA2_ERR_DEVICE_BOUNDS, kKMass, x.b, x.key);
       return -1;
     };
-    const uint8_t *cp = cache.kv_codes, *sp = cache.kv_scales;   // of the tile to be loaded
+    const uint8_t* cp = kMStages > 0 ? S.stage : cache.kv_codes;   // of the tile to be loaded
+    const uint8_t* sp = kMStages > 0 ? S.stage : cache.kv_scales;
     uint32_t next_mask = 0;
     auto aim = [&](int base) {
       const long long r = max(base, 0) + krow;       // entries that are not there read row 0 with a scale of 0
@@ -490,24 +499,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       }
       return true;
     };
-    bool have = next_tile_of(), more = false;        // a tile is loaded; another one comes after it
-    Place ahead = {};
-    if (have) {
-      aim(row_of_page(fetch(tb, tctx, tile)));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) load(i);
-      mask = next_mask;
-      more = next_tile_of();
-      if (more) ahead = fetch(tb, tctx, tile);
-    }
     int n = 0;                                       // the next pair in the order of all pairs
-    while (ok && have) {
-      have = more;
-      if (more) {
-        aim(row_of_page(ahead));
-        more = next_tile_of();
-        if (more) ahead = fetch(tb, tctx, tile);
-      }
+    // The held granules into the four pairs of slots in turn; their registers
+    // then receive those of the tile that is aimed at.
+    auto store_tile = [&](bool then_load) {
 #pragma unroll
       for (int p = 0; p < 4; ++p, ++n) {
         const int x2 = n % kMRing;
@@ -522,13 +517,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(dst + i * 64 * 128 + (((kg * 4 + j) ^ (krow & 7)) << 4)) = o[j];
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) load(2 * p + i); // the next tile's (at the end: the last one's again)
+        if (then_load) load(2 * p), load(2 * p + 1);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.full[x2]), 0));
       }
       mask = next_mask;
+    };
+    if constexpr (kMStages == 0) {
+      bool have = next_tile_of(), more = false;      // a tile is loaded; another one comes after it
+      Place ahead = {};
+      if (have) {
+        aim(row_of_page(fetch(tb, tctx, tile)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(i);
+        mask = next_mask;
+        more = next_tile_of();
+        if (more) ahead = fetch(tb, tctx, tile);
+      }
+      while (ok && have) {
+        have = more;
+        if (more) {
+          aim(row_of_page(ahead));
+          more = next_tile_of();
+          if (more) ahead = fetch(tb, tctx, tile);
+        }
+        store_tile(true);                            // (at the end the last tile is loaded again)
+      }
+    } else {
+      // The first warp walks over the tiles and has each one's packed rows (128
+      // neighbours of one page) copied to a stage, kMStages tiles ahead of the
+      // registers; a stage says what it holds, so the other warps need no walk.
+      const bool walker = warp == kMEpiWarps;
+      const uint64_t policy = l2_policy_evict_first();
+      bool more = false;
+      Place ahead = {};
+      int issued = 0, t = 0;                         // tiles asked for, tiles taken
+      auto issue = [&]() {
+        const int st = issued++ % kMStages;
+        int base = -2;
+        if (more) {
+          base = row_of_page(ahead);
+          more = next_tile_of();
+          if (more) ahead = fetch(tb, tctx, tile);
+        }
+        if (lane == 0) {
+          S.stage_row[st] = base;
+          if (base >= 0) {
+            uint8_t* dst = S.stage + st * kMStage;
+            mbar_arrive_expect_tx(&S.stage_full[st], kMStage);
+            bulk_load_1d(dst, cache.kv_codes + static_cast<long long>(base) * kKvCodeBytes, 128 * kKvCodeBytes,
+                         &S.stage_full[st], policy);
+            bulk_load_1d(dst + 128 * kKvCodeBytes, cache.kv_scales + static_cast<long long>(base) * kKvScaleBytes,
+                         128 * kKvScaleBytes, &S.stage_full[st], policy);
+          } else {
+            mbar_arrive(&S.stage_full[st]);
+          }
+        }
+        __syncwarp();
+      };
+      bool next = false;                             // the tile that is aimed at exists
+      auto take = [&]() {
+        const int st = t % kMStages;
+        ok = mbar_wait_all(&S.stage_full[st], (t / kMStages) & 1, wait_ns);
+        const int base = ok ? *reinterpret_cast<volatile int*>(&S.stage_row[st]) : -2;
+        next = base != -2;
+        next_mask = base < 0 ? 0u : 0x7F7Fu;
+        cp = S.stage + st * kMStage + krow * kKvCodeBytes + k_code;
+        sp = S.stage + st * kMStage + 128 * kKvCodeBytes + krow * kKvScaleBytes + k_sc;
+      };
+      auto give = [&]() {                            // every warp has read the stage (or one gave up: all do)
+        ok = !named_bar_or(kBarDeq, kMDeqWarps * 32, !ok);
+        if (ok) ++t;
+        if (ok && walker && next) issue();
+      };
+      if (walker) {
+        more = next_tile_of();
+        if (more) ahead = fetch(tb, tctx, tile);
+        for (int i = 0; i < kMStages; ++i) issue();
+      }
+      take();
+      if (next) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load(i);
+      }
+      mask = next_mask;
+      bool have = next;
+      give();
+      while (ok && have) {
+        take();
+        have = next;
+        store_tile(next);
+        give();
+      }
+      // copies that were asked for and not awaited
+      if (!ok && walker)
+        for (; t < issued; ++t) (void)mbar_wait_all(&S.stage_full[t % kMStages], (t / kMStages) & 1, kWaitLimitNs);
     }
     if (!ok && lane == 0) report_error(cache.err_word, CSA2_ERR_TIMEOUT, kKMass, static_cast<int>(rank), -n);
   } else if (rank == 0) {
@@ -561,11 +645,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (issue) {
-            const uint64_t ad = k_desc + s * (2 * kMSlot / 16), bd = q_desc + c * (2 * kMSlot / 16);
+            const uint64_t ad = k_desc + s * (2 * kMSlot / 16), bd = q_desc + c * (2 * kMQPart / 16);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               umma_f16_pair(tmem + acc * kMRows, ad + (kk >> 2) * (kMSlot / 16) + (kk & 3) * 2,
-                            bd + (kk >> 2) * (kMSlot / 16) + (kk & 3) * 2, idesc, (c | kk) > 0 ? 1u : 0u);
+                            bd + (kk >> 2) * (kMQPart / 16) + (kk & 3) * 2, idesc, (c | kk) > 0 ? 1u : 0u);
             umma_commit_pair(&S.empty[s]);
             if (c == 3) {
               umma_f16_pair(tmem + acc * kMRows, ones_desc, lse_desc, idesc, 1u);
@@ -617,6 +701,20 @@ __global__ void __launch_bounds__(kMKeys) attn_mass_join_kernel(const csa2_cache
   if (sum != 0.0f) mass[r.b * capacity + key] += sum;
 }
 
+template <int kMRows, int kMRing, int kMStages>
+cudaError_t launch_mass(const DenseArgs& a, const __nv_bfloat16* q, float scale, const float* lse, float* mass, void* ws,
+                        int pairs, uint64_t wait_ns, cudaStream_t stream) {
+  static ContextMemo attrs;
+  const size_t smem = sizeof(MassSmem<kMRows, kMRing, kMStages>) + 1024;
+  const cudaError_t e = attrs.once([&] {
+    return cudaFuncSetAttribute(attn_mass_kernel<kMRows, kMRing, kMStages>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem));
+  });
+  if (e != cudaSuccess) return e;
+  attn_mass_kernel<kMRows, kMRing, kMStages><<<2 * pairs, kMThreads, smem, stream>>>(a, q, scale, lse, mass, ws, wait_ns);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t attn_mass_workspace_bytes() {
@@ -626,17 +724,15 @@ size_t attn_mass_workspace_bytes() {
 cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32_t* q_start, const int32_t* q_pos,
                              int ratio, const uint16_t* q, int H, float scale, const float* lse, float* mass, void* ws,
                              int num_sms, uint64_t wait_ns, cudaStream_t stream) {
-  static ContextMemo attrs;
-  const size_t smem = sizeof(MassSmem) + 1024;
-  cudaError_t e = attrs.once([&] {
-    return cudaFuncSetAttribute(attn_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  });
-  if (e != cudaSuccess) return e;
   const DenseArgs a = {cache, q_start, q_pos, n_queries, ratio, H, 1};
   const int pairs = min(kMaxPairs, num_sms / 2);
-  attn_mass_kernel<<<2 * pairs, kMThreads, smem, stream>>>(a, reinterpret_cast<const __nv_bfloat16*>(q), scale, lse, mass,
-                                                           ws, wait_ns);
-  e = cudaGetLastError();
+  // Few rows a request (single tokens): tiles of 64 rows, whose place in shared
+  // memory three more pairs of slots take; a request with more rows among them
+  // streams its entries once per 64.  MEASURED
+  const bool narrow = static_cast<long long>(n_queries) * H <= 64LL * cache.batch;
+  const __nv_bfloat16* q16 = reinterpret_cast<const __nv_bfloat16*>(q);
+  cudaError_t e = narrow ? launch_mass<64, 3, 2>(a, q16, scale, lse, mass, ws, pairs, wait_ns, stream)
+                         : launch_mass<256, 2, 0>(a, q16, scale, lse, mass, ws, pairs, wait_ns, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pairs, kMPart);

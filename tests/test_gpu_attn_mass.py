@@ -233,3 +233,39 @@ def test_attn_mass_wait_limit(csa2):  # noqa: F811
     st, word = csa2.get_error(cache)
     assert st == csa2.OK, word
     _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
+@pytest.mark.parametrize("H,new", [(16, [0, 12, 1, 0, 0, 3]), (64, [0, 0, 4, 0, 1, 0]), (32, [11, 0, 0, 0, 0, 0])])
+def test_attn_mass_few_rows_unevenly(csa2, H, new):  # noqa: F811
+    """Few query rows per request on average, most of them one request's."""
+    lens = [100, 9000, 2600, 5, 700, 33]
+    lens[0] = 8300 if new[0] else 100
+    case = _case(csa2, lens, new, H, 128, seed=H, pad=1)
+    cache, _, _, _, start, pos, q = case
+    assert q.shape[0] * H <= 64 * len(lens)
+    lse, want, tol = _reference(case, lens, 1, 1 / math.sqrt(512))
+    mass = torch.zeros(cache.batch, cache.capacity, device="cuda")
+    csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(start).cuda())
+    st, word = csa2.get_error(cache)
+    assert st == csa2.OK, word
+    _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
+def test_attn_mass_wait_limit_single_tokens(csa2):  # noqa: F811
+    lens = [3000, 200]
+    case = _case(csa2, lens, [1, 1], 32, 128, seed=3)
+    cache, _, _, _, _, pos, q = case
+    lse, want, tol = _reference(case, lens, 1, 1 / math.sqrt(512))
+    p = torch.from_numpy(pos).cuda()
+    csa2.set_wait_limit_ns(0)
+    try:
+        csa2.attn_mass(cache, q, p, lse, torch.zeros(2, cache.capacity, device="cuda"))
+        st, _ = csa2.get_error(cache)
+    finally:
+        csa2.set_wait_limit_ns(2_000_000_000)
+    assert st == csa2.ERR_TIMEOUT
+    cache.err_word.zero_()
+    mass = csa2.attn_mass(cache, q, p, lse, torch.zeros(2, cache.capacity, device="cuda"))
+    st, word = csa2.get_error(cache)
+    assert st == csa2.OK, word
+    _check(mass, torch.zeros_like(mass), want, tol, lens)

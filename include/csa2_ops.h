@@ -135,7 +135,7 @@ CSA2_API csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries,
  *   mass     float [batch][capacity], added to (zero it once); entries that no
  *            query of the call sees are untouched
  *   workspace  at least csa2_attn_mass_workspace_bytes bytes, as above
- * fp32 sums in an order fixed by the lengths.  Device errors as
+ * fp32 sums in an order fixed by the sizes and lengths.  Device errors as
  * csa2_chunk_attn; a pipeline wait that runs out -> CSA2_ERR_TIMEOUT (mass is
  * then undefined).
  */

@@ -11,6 +11,9 @@
 //     into a ring of two 32 KB pairs of slots.  Entries are 288 bytes each where
 //     a query row is 1 KB, so this is the side to stream; for single tokens it
 //     is the only one that is long.
+//   * With few rows a request the tile is 64 rows (32 per CTA, 32 KB), and packed
+//     entries come by bulk copies, two tiles ahead in shared memory: loads into
+//     registers kept 36 KB an SM under way, too few for entries from HBM.
 //   * The rows' log-sum-exp is taken off by the product itself: one more step of
 //     K holds ones for the entries and -lse, in three fp16 parts, for the rows.  It
 //     comes last, where the sum is small.  So the epilogue needs nothing per
@@ -26,6 +29,11 @@
 // request, part of 8,192 entries, row tile, tile of entries: a pair holds a
 // part's sums in shared memory over all row tiles.  Parts that ranges cut are
 // joined in a fixed order by a second launch.
+//
+// 512 tokens x 64 heads of two requests over 16,384 entries: 0.95 ms, 0.69 of the
+// tensor cores' measured rate; 8 single tokens x 64 heads over 65,536: 91 us.
+// What bounds it is the dequantisation (5,000 to 7,000 cycles for a tile's 128
+// entries a CTA, against 4,096 of products with 256 rows).
 #include <cuda_bf16.h>
 
 #include "launch.h"
@@ -726,9 +734,11 @@ cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32
                              int num_sms, uint64_t wait_ns, cudaStream_t stream) {
   const DenseArgs a = {cache, q_start, q_pos, n_queries, ratio, H, 1};
   const int pairs = min(kMaxPairs, num_sms / 2);
-  // Few rows a request (single tokens): tiles of 64 rows, whose place in shared
-  // memory three more pairs of slots take; a request with more rows among them
-  // streams its entries once per 64.  MEASURED
+  // At most 64 query rows a request on average (single tokens): tiles of 64 rows,
+  // and the room in shared memory for stages of packed entries and a third pair
+  // of slots.  One token of 8 requests x 64 heads over 65,536 entries: 91 us, with
+  // tiles of 256 rows 104; with 128 rows a request the narrow tiles read the
+  // entries twice: 166 us against 121 (8 x 2 tokens x 64 heads over 65,536).
   const bool narrow = static_cast<long long>(n_queries) * H <= 64LL * cache.batch;
   const __nv_bfloat16* q16 = reinterpret_cast<const __nv_bfloat16*>(q);
   cudaError_t e = narrow ? launch_mass<64, 3, 2>(a, q16, scale, lse, mass, ws, pairs, wait_ns, stream)

@@ -52,7 +52,7 @@ typedef struct csa2_rope {
  *   pos       int32 [n_rows] position of each row (any value)
  *   out       [n_rows][heads][dim] of out_type, contiguous, 16-byte aligned.
  *             It may be x itself when the type and the layout are the same;
- *             it must not overlap x in any other way.
+ *             any other overlap with x is refused.
  * A row that holds a NaN or an infinity follows the formula (NaN where the
  * value is not finite, 0 or NaN elsewhere).
  */
@@ -102,7 +102,7 @@ CSA2_API csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_i
  *            nothing; any order)
  *   ratio    tokens per entry, >= 1
  *   q, out   bf16 [n_queries][H][512], 16-byte aligned; H in {16, 32, 64}.
- *            out must not overlap q
+ *            An out that overlaps q is refused
  *   lse      float [n_queries][H] or NULL
  *   n_queries <= 2^20
  *   workspace  at least csa2_chunk_attn_workspace_bytes bytes, 16-byte

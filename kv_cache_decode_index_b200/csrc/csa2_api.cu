@@ -182,6 +182,12 @@ csa2_status check_dense(const csa2_cache* c, int n_queries, const int32_t* q_sta
   return CSA2_OK;
 }
 
+// Whether [a, a + a_bytes) and [b, b + b_bytes) meet.
+bool overlap(const void* a, unsigned long long a_bytes, const void* b, unsigned long long b_bytes) {
+  const unsigned long long x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 csa2_status check_workspace(const void* ws, size_t bytes, size_t need, const char* fn) {
   if (ws == nullptr || !aligned(ws, 16)) return fail(CSA2_ERR_ARG, "workspace must be set and 16-byte aligned");
   if (bytes < need) return fail(CSA2_ERR_SHAPE, "workspace_bytes %zu < %zu (%s)", bytes, need, fn);
@@ -603,6 +609,10 @@ csa2_status csa2_norm_rope(int32_t n_rows, int32_t heads, int32_t dim, const voi
   if (n_rows == 0) return CSA2_OK;
   if (x == nullptr || out == nullptr || pos == nullptr || !aligned(x, 16) || !aligned(out, 16) || !aligned(weight, 16))
     return fail(CSA2_ERR_ARG, "x, out (16-byte aligned) and pos must be set, weight 16-byte aligned");
+  const unsigned long long row = static_cast<unsigned long long>(heads) * dim, xs = x_type == CSA2_BF16 ? 2 : 4;
+  const bool in_place = out == x && out_type == x_type && (n_rows == 1 || static_cast<unsigned long long>(x_stride) == row);
+  if (!in_place && overlap(x, ((n_rows - 1ull) * x_stride + row) * xs, out, n_rows * row * (out_type == CSA2_BF16 ? 2 : 4)))
+    return fail(CSA2_ERR_ARG, "out overlaps x without being x");
   DeviceInfo d;
   CSA2_TRY(device_info(&d));
   const cudaError_t e = csa2::launch_norm_rope(n_rows, heads, dim, x, x_type, x_stride, weight, eps, *rope, pos, out,
@@ -652,6 +662,8 @@ csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries, const in
     return fail(CSA2_ERR_ARG, "q_pos, q and out (16-byte aligned) must be set");
   CSA2_TRY(check_workspace(workspace, workspace_bytes, csa2_chunk_attn_workspace_bytes(cache->batch, n_queries, H),
                            "csa2_chunk_attn_workspace_bytes"));
+  const unsigned long long bytes = 2ull * n_queries * H * csa2::kKvDim;
+  if (overlap(q, bytes, out, bytes)) return fail(CSA2_ERR_ARG, "out overlaps q");
   DeviceInfo d;
   CSA2_TRY(device_info(&d));
   const cudaError_t e = csa2::launch_chunk_attn(*cache, n_queries, q_start, q_pos, ratio, q, H, scale, out, lse, workspace,

@@ -29,6 +29,14 @@
 // The running maximum is raised only when a row's new maximum is more than 2^8
 // above it (the probabilities stay below 2^8 until then, well inside fp16), so
 // that O, which lies in tensor memory, is rarely rescaled.
+//
+// 1,024 tokens x 64 heads over 32,768 entries: 3.85 ms, 0.67 of the tensor cores'
+// measured rate; one token of 8 requests x 64 heads over 65,536: 160 us with the
+// join.  A step of 256 keys takes 6,800 to 7,500 cycles against 4,096 of
+// products; what bounds it is the shared-memory pipe (72 % of its wavefronts are
+// taken: two dequantised operands, the probabilities, the score tiles).
+// Taking the maximum and the probabilities in one pass over the score tile, with
+// a repeat when a maximum rises, was slower (4.11 ms).
 #include <cuda_bf16.h>
 #include <stddef.h>
 

@@ -123,3 +123,20 @@ def test_evict_refusals(lib):  # noqa: F811
     assert call(out=P) == lib.ERR_ARG and call(new_len=P) == lib.ERR_ARG and call(dst=P) == lib.ERR_ARG
     assert call(ws=None) == lib.ERR_ARG and call(size=need - 1) == lib.ERR_SHAPE
     assert call(ik4=ctypes.byref(lib.Ik4Struct(None, None))) == lib.ERR_ARG
+
+
+def test_overlapping_outputs_are_refused(lib):  # noqa: F811
+    c, p = _cache(lib)
+    V = ctypes.c_void_p
+    f = lib._lib.csa2_chunk_attn
+    need = lib._lib.csa2_chunk_attn_workspace_bytes(2, 2, 16)
+    size = 2 * 16 * 512 * 2
+    for out in (p, p + 16, p - 16, p + size - 16, p - size + 16):
+        assert f(ctypes.byref(c), 2, V(p), V(p), 1, V(p), 16, F32(0.1), V(out), None, V(p), need, None) == lib.ERR_ARG
+        assert b"overlaps" in lib._lib.csa2_last_error_message()
+    f, rope = lib._lib.csa2_norm_rope, lib.RopeStruct(p, 64, 1)
+    # rows of 2 x 128 bf16, 512 bytes each; x two rows, out bf16 or fp32
+    for stride, out, ot in ((264, p, 0), (256, p, 1), (256, p + 16, 0), (256, p - 1008, 0), (256, p - 2032, 1),
+                            (264, p + 1024, 0)):
+        assert f(2, 2, 128, V(p), 0, stride, None, F32(1e-6), ctypes.byref(rope), V(p), V(out), ot, None) == lib.ERR_ARG
+        assert b"overlaps" in lib._lib.csa2_last_error_message()

@@ -11,11 +11,11 @@
 // Both products take the dequantised row as operand B, once with the channels
 // as K (K-major) and once with the keys as K (MN-major).  tcgen05 over a pair
 // has each CTA hold one half of B's N: its 128 keys of the tile for S, its 256
-// neighbouring channels of every key for O.  Why a pair with M = 128: 512 output channels of
-// 128 rows in fp32 are a whole SM's tensor memory; over a pair they take half
-// of each (256 columns), which leaves room for two score tiles (2 x 128), and
-// N = 256 keeps the full rate that M = 128 has over a pair (64 cycles per MMA
-// of K = 16; N = 128 takes 47, no less than N = 64).
+// neighbouring channels of every key for O.  Why a pair with M = 128: 512 output
+// channels of 128 rows in fp32 are a whole SM's tensor memory; over a pair they
+// take half of each (256 columns), which leaves room for two score tiles (2 x
+// 128), and N = 256 keeps the full rate that M = 128 has over a pair (64 cycles
+// per MMA of K = 16; N = 128 takes 47, no less than N = 64).
 //
 // Roles: warps 0-3 softmax (thread = row and half of the tile's keys), warps
 // 4-11 dequantisation (packed rows from L2 into registers one half tile ahead,

@@ -105,10 +105,12 @@ __device__ __forceinline__ int dense_steps(const DenseTile& t) {
   return max(1, (t.keys + kStep - 1) / kStep);   // a tile that sees nothing still writes its rows
 }
 
-// Starting and ending a tile costs about as much as two of its steps, so the
-// plan counts kTileCost steps more for each, before its own: with none a range
-// of many short tiles took twice as long as the others.
-constexpr int kTileCost = 2;
+// Starting and ending a tile (queries, first products, output rows) costs about
+// as much as three of its steps, so the plan counts kTileCost steps more for
+// each, before its own.  A ragged batch (6 requests, up to 333 new tokens x 32
+// heads over up to 7,001 entries) by its value, 0 to 4: 419, 314, 257, 245, 247
+// us; long prompts and equal requests hardly depend on it.
+constexpr int kTileCost = 3;
 // The part [first, first + n) of a tile's own steps that lies in a range which
 // starts `off` counted steps into the tile and has `left` left; n may be 0.
 struct TilePart {

@@ -7,7 +7,9 @@
  * The conventions of csa2.h hold: device pointers owned by the caller, host
  * validation before any launch, no allocation or synchronisation, work
  * enqueued on `stream`, data-dependent violations recorded in
- * cache->err_word and never trapping.
+ * cache->err_word and never trapping.  csa2_chunk_attn, csa2_attn_mass and
+ * csa2_evict take caches of up to 2^30 entries a request (max_pages_per_req *
+ * page_size).
  */
 #ifndef CSA2_OPS_H
 #define CSA2_OPS_H
@@ -153,7 +155,7 @@ CSA2_API csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, 
  * in their old order: the new cache is the old one without the others.
  * Requests with n <= budget are left where they are.
  *   mass       float [batch][capacity] (from csa2_attn_mass)
- *   budget     >= 1; sink, recent >= 0, sink + recent <= budget
+ *   budget     1 .. 2^30; sink, recent >= 0, sink + recent <= budget
  *   dst_pages  int32 [batch][dst_width]: the pages that receive a request's
  *              rows (dst_width * page_size >= budget; entries of requests that
  *              are left alone are not read).  They must be free: a page that

@@ -144,6 +144,7 @@ csa2_status check_cache(const csa2_cache* c, bool need_kv, bool need_ik) {
 
 constexpr int kMaxNormHeads = 4096;
 constexpr int kMaxDenseQueries = 1 << 20;
+constexpr long long kMaxOpsCapacity = 1 << 30;   // entries a request: positions plus a page or a tile stay in 32 bits
 
 csa2_status check_dtype(csa2_dtype t) {
   return t == CSA2_BF16 || t == CSA2_F32 ? CSA2_OK : fail(CSA2_ERR_ARG, "unknown element type %d", static_cast<int>(t));
@@ -169,9 +170,16 @@ csa2_status check_stride(long long stride, long long width, csa2_dtype t, const 
   return CSA2_OK;
 }
 
+csa2_status check_ops_capacity(const csa2_cache* c) {
+  if (capacity_of(c) > kMaxOpsCapacity)
+    return fail(CSA2_ERR_SHAPE, "max_pages_per_req * page_size must be at most 2^30 here");
+  return CSA2_OK;
+}
+
 // What the dense operators (chunk_attn, attn_mass) share.
 csa2_status check_dense(const csa2_cache* c, int n_queries, const int32_t* q_start, int ratio, int H, float scale) {
   CSA2_TRY(check_cache(c, true, false));
+  CSA2_TRY(check_ops_capacity(c));
   if (n_queries < 0 || n_queries > kMaxDenseQueries)
     return fail(CSA2_ERR_SHAPE, "n_queries %d outside [0, %d]", n_queries, kMaxDenseQueries);
   if (q_start == nullptr && n_queries > c->batch)
@@ -701,7 +709,8 @@ csa2_status csa2_evict(const csa2_cache* cache, const csa2_ik4* ik4, const float
                        float* mass_out, void* workspace, size_t workspace_bytes, void* stream) {
   CSA2_TRY(check_cache(cache, true, true));
   if (ik4 != nullptr) CSA2_TRY(check_ik4(ik4));
-  if (budget < 1) return fail(CSA2_ERR_SHAPE, "budget %d < 1", budget);
+  CSA2_TRY(check_ops_capacity(cache));
+  if (budget < 1 || budget > kMaxOpsCapacity) return fail(CSA2_ERR_SHAPE, "budget %d outside [1, 2^30]", budget);
   if (sink < 0 || recent < 0 || static_cast<long long>(sink) + recent > budget)
     return fail(CSA2_ERR_SHAPE, "sink %d and recent %d must be >= 0 and together at most the budget (%d)", sink, recent, budget);
   if (dst_width < 1 || static_cast<long long>(dst_width) * cache->page_size < budget)

@@ -140,3 +140,22 @@ def test_overlapping_outputs_are_refused(lib):  # noqa: F811
                             (264, p + 1024, 0)):
         assert f(2, 2, 128, V(p), 0, stride, None, F32(1e-6), ctypes.byref(rope), V(p), V(out), ot, None) == lib.ERR_ARG
         assert b"overlaps" in lib._lib.csa2_last_error_message()
+
+
+def test_capacities_above_2_30_are_refused(lib):  # noqa: F811
+    """Positions plus a tile or a page would leave 32 bits."""
+    V = ctypes.c_void_p
+    c, p = _cache(lib, page_size=2 ** 20, num_pages=4, max_pages_per_req=1025)
+    need = lib._lib.csa2_chunk_attn_workspace_bytes(2, 2, 16)
+    assert lib._lib.csa2_chunk_attn(ctypes.byref(c), 2, V(p), V(p), 1, V(p), 16, F32(0.1), V(p + 2 ** 20), None, V(p), need,
+                                    None) == lib.ERR_SHAPE
+    need = lib._lib.csa2_attn_mass_workspace_bytes(2, 2, 16)
+    assert lib._lib.csa2_attn_mass(ctypes.byref(c), 2, V(p), V(p), 1, V(p), 16, F32(0.1), V(p), V(p), V(p), need,
+                                   None) == lib.ERR_SHAPE
+    evict = lambda cache, budget: lib._lib.csa2_evict(  # noqa: E731
+        ctypes.byref(cache), None, V(p), budget, 1, 9, V(p + 1024), 2047, V(p + 512), V(p + 512), None, V(p), 16, None)
+    assert evict(c, 100) == lib.ERR_SHAPE
+    assert b"2^30" in lib._lib.csa2_last_error_message()
+    c, _ = _cache(lib, page_size=2 ** 20, num_pages=4, max_pages_per_req=1024)
+    assert evict(c, 2 ** 30 + 1) == lib.ERR_SHAPE
+    assert b"2^30" in lib._lib.csa2_last_error_message()

@@ -66,10 +66,7 @@ struct __align__(1024) MassSmem {
   uint8_t q[kKvDim / 64][kMRows / 2 * 128];       // B: this CTA's half of the rows, 64 channels a part
   union {
     uint8_t ring[kMRing][2 * kMSlot];             // A: 128 entries, 128 channels a pair
-    struct {                                      // plan, before the first pair is filled
-      int ctx[kMaxDenseBatch];
-      long long at[kMaxDenseBatch + 1];           // steps before each request
-    };
+    long long at[kMaxDenseBatch + 1];             // plan, before the first pair is filled: steps before each request
   };
   uint8_t a_ones[128 * 32];                       // the last step of K: A ...
   uint8_t b_lse[128 * 32];                        // ... and B
@@ -143,7 +140,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
   for (int b = tid; b < cache.batch; b += kMThreads) {
     const int n = queries_of(a, b, kKMass, blockIdx.x == 0);
     const int ctx = n > 0 ? max(0, checked_ctx_len(cache, b, capacity, kKMass, blockIdx.x == 0)) : 0;
-    S.ctx[b] = ctx;
     S.at[b + 1] = static_cast<long long>((ctx + kMKeys - 1) / kMKeys) *
                   ((static_cast<long long>(n) * a.heads + kMRows - 1) / kMRows);
   }

@@ -166,3 +166,65 @@ def test_prompt_eviction_and_decode(csa2, H, lens, budget):  # noqa: F811
             K[b] = np.concatenate([K[b], new[b:b + 1]])
             check_attention(q1[b:b + 1], K[b], [len(K[b])], out1[b:b + 1], lse1[b:b + 1], mass[b], before[b])
     np.testing.assert_array_equal(cache.ctx_len.cpu().numpy(), [v + steps for v in lens2])
+
+
+def test_two_streams_and_a_shared_workspace_in_turn(csa2):  # noqa: F811
+    """Calls of two streams in flight at once (a workspace each), and two
+    graphs that use one workspace one after the other: the bits are those of
+    single calls, whatever a workspace held before."""
+    H, lens, new = 32, [1500, 700, 2600], [40, 1, 9]
+    cache, _, _, _ = O.random_cache(csa2, lens, 128, seed=21)
+    rng = np.random.default_rng(22)
+    c = lambda a: torch.from_numpy(np.asarray(a, np.int32)).cuda()  # noqa: E731
+    start = np.concatenate([[0], np.cumsum(new)])
+    cases = []
+    for k in range(2):
+        pos = c(np.concatenate([rng.integers(0, n, x) for n, x in zip(lens, new)]))
+        q = torch.from_numpy(rng.standard_normal((sum(new), H, 512)).astype(np.float32)).bfloat16().cuda() * 0.2
+        cases.append((pos, q, torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"),
+                      torch.empty(3, cache.capacity, device="cuda"),
+                      torch.empty(max(csa2.chunk_attn_workspace_bytes(cache, sum(new), H),
+                                      csa2.attn_mass_workspace_bytes(cache, sum(new), H)), dtype=torch.uint8,
+                                  device="cuda")))
+    st = c(start)
+
+    def run(k, ws):
+        pos, q, out, lse, mass, _ = cases[k]
+        csa2.chunk_attn(cache, q, pos, st, out=out, lse=lse, workspace=ws)
+        mass.zero_()
+        csa2.attn_mass(cache, q, pos, lse, mass, st, workspace=ws)
+
+    def results(k):
+        return [t.clone() for t in cases[k][2:5]]
+
+    want = []
+    for k in range(2):
+        run(k, cases[k][5])
+        want.append(results(k))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for k in range(2):
+            cases[k][2].zero_(), cases[k][3].zero_()
+        torch.cuda.synchronize()
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                run(k, cases[k][5])
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(want[k], results(k)))
+    shared = cases[0][5]
+    graphs = []
+    for k in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[k]):
+            run(k, shared)
+    for order in ((0, 1), (1, 0), (1, 1, 0)):
+        shared.fill_(0xFF)
+        for k in order:
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(want[k], results(k)))
+    status, word = csa2.get_error(cache)
+    assert status == csa2.OK, word

@@ -228,3 +228,39 @@ def test_two_streams_and_a_shared_workspace_in_turn(csa2):  # noqa: F811
             assert all(torch.equal(a, b) for a, b in zip(want[k], results(k)))
     status, word = csa2.get_error(cache)
     assert status == csa2.OK, word
+
+
+def test_rows_behind_32_bit_offsets(csa2):  # noqa: F811
+    """A cache of 17.2 million rows (codes behind 2^32 bytes): the bits are
+    those of a small cache with the same rows."""
+    page, H, lens = 4096, 16, [5000, 130]
+    small = csa2.Cache(5, page, [[0, 1], [2, -1]], lens)
+    P = 4200
+    assert (P - 5) * page * 256 > 2 ** 32
+    big = csa2.Cache(P, page, [[P - 1, P - 4], [P - 2, -1]], lens)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = sum(lens)
+    x = torch.randn(n, 640, generator=g, device="cuda")
+    pos = torch.cat([torch.arange(v) for v in lens]).int().cuda()
+    req = torch.repeat_interleave(torch.arange(2), torch.tensor(lens)).int().cuda()
+    q = torch.randn(2, H, 512, generator=g, device="cuda").bfloat16()
+    qp = torch.tensor(lens).int().cuda() - 1
+    rope = csa2.Rope(torch.from_numpy(O.freqs(ROT)).cuda())
+    results = []
+    for cache, dst in ((small, [[3], [-1]]), (big, [[P - 3], [-1]])):
+        k4 = csa2.Ik4(cache)
+        csa2.norm_rope_append(cache, x[:, :512], x[:, 512:], pos, rope, rope, req=req, ik4=k4)
+        lse = torch.empty(2, H, device="cuda")
+        out = csa2.chunk_attn(cache, q, qp, lse=lse)
+        mass = csa2.attn_mass(cache, q, qp, lse, torch.zeros(2, cache.capacity, device="cuda"))
+        dst = torch.tensor(dst).int().cuda()
+        kept, new_len = csa2.evict(cache, mass, 1000, dst, sink=4, recent=16, ik4=k4)
+        st, word = csa2.get_error(cache)
+        assert st == csa2.OK, word
+        row = int(dst[0, 0]) * page
+        results.append([out, lse, mass, kept, new_len, cache.kv_codes[row:row + 1000], cache.kv_scales[row:row + 1000],
+                        cache.ik_codes[row:row + 1000], cache.ik_exp[row:row + 1000], k4.codes[row:row + 1000],
+                        k4.scales[row // 128:row // 128 + 7]])
+    assert int(results[0][5].sum()) > 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b)

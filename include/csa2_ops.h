@@ -115,11 +115,11 @@ CSA2_API csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_i
  * cut along the keys by a plan made of the lengths alone: the same lengths
  * give the same bits.
  * Device errors: a page id outside [0, num_pages) under a visible entry
- * (CSA2_ERR_DEVICE_BOUNDS; its entries are left out), a q_start that
- * decreases or leaves [0, n_queries] (the request has no queries), a ctx_len
- * outside [0, capacity] (its queries see nothing); a pipeline wait that runs
- * out -> CSA2_ERR_TIMEOUT (out and lse are then undefined; see
- * csa2_set_wait_limit_ns).
+ * (CSA2_ERR_DEVICE_BOUNDS; its entries are left out, as if the query did not
+ * see them), a q_start that decreases or leaves [0, n_queries] (the request has
+ * no queries), a ctx_len outside [0, capacity] (its queries see nothing); a
+ * pipeline wait that runs out -> CSA2_ERR_TIMEOUT (out and lse are then
+ * undefined; see csa2_set_wait_limit_ns).
  */
 CSA2_API size_t csa2_chunk_attn_workspace_bytes(int32_t batch, int32_t n_queries, int32_t H);
 CSA2_API csa2_status csa2_chunk_attn(const csa2_cache* cache, int32_t n_queries, const int32_t* q_start,

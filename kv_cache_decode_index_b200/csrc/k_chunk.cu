@@ -222,7 +222,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       // (a lane without a row follows the tile's keys: with 0 it would hold its
       // warp to the masked form at every tile)
       const bool real = own < rows;
-      const int lim = real ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : T.keys;
+      const int seen_keys = real ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : T.keys;
+      // A tile's keys of this thread lie on one page; its id is looked up a tile
+      // ahead.  Keys under a bad one take no part (the dequantisation records it).
+      auto page_of = [&](int t) {
+        const int key = (first + t) * kGKeys + khalf * 128;
+        return key < T.keys ? cache.page_table[static_cast<long long>(T.b) * cache.max_pages_per_req + key / cache.page_size]
+                            : 0;
+      };
+      int page = page_of(0);
       load_query_rows<kGRows, kGSoftWarps, kPerRow>(q, static_cast<long long>(T.q0) * a.heads + static_cast<int>(rank) * kGRows,
                                            rows - static_cast<int>(rank) * kGRows, kGRows, sign, S.q[0], warp, lane,
                                            [&](int r, uint32_t top) {
@@ -236,6 +244,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 
       for (int t = 0; t < seg; ++t, ++g) {
         const int key0 = (first + t) * kGKeys + khalf * 128;
+        const int lim = page >= 0 && page < cache.num_pages ? seen_keys : min(seen_keys, key0);
+        page = page_of(t + 1);                       // (nothing is read behind the tile's keys)
         const uint32_t s_addr = tmem + lane_base + kSCol + (g & 1) * 128;
         if (!mbar_wait_all(&S.s_full[g & 1], (g >> 1) & 1, wait_ns)) ok = false;
         ok = !named_bar_or(kBarSoft, kGSoftWarps * 32, !ok || S.abort_flag != 0);

@@ -240,3 +240,53 @@ def test_chunk_attn_wait_limit(csa2):  # noqa: F811
     st, word = csa2.get_error(cache)
     assert st == csa2.OK, word
     _check(*args, out, lse, [2000, 300], 1, 1 / math.sqrt(512))
+
+
+def _without(table, page, n_ctx, bad):
+    """Entries of a request that do not lie under the bad page slots."""
+    return np.nonzero(~np.isin(np.arange(n_ctx) // page, bad))[0]
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("q_scale", [1.0, 4.0])
+@pytest.mark.parametrize("lens,new,page,bad", [
+    ([300, 200], [70, 3], 128, [[1], []]),              # the second half of the first tile
+    ([1000, 700], [40, 300], 256, [[0], [2]]),          # a whole tile, the first one; the last entries
+    ([900, 130], [1, 130], 384, [[1], [0]]),            # pages that end inside a tile; nothing is left
+    ([6000, 200], [1, 1], 128, [list(range(4, 30)), []]),   # ranges of a cut request in which nothing is left
+])
+def test_chunk_attn_leaves_bad_pages_out(csa2, lens, new, page, bad, q_scale, H):
+    """Entries under a page id out of range take no part in the softmax, as if
+    they were not there; the weights (attn_mass) of the others sum to the
+    queries that see something."""
+    args = _case(csa2, lens, new, H, page, seed=7, q_scale=q_scale)
+    cache, table, codes, scales, start, pos, q = args
+    for b, slots in enumerate(bad):
+        for i, s in enumerate(slots):
+            cache.page_table[b, s] = (-1, cache.num_pages, -2 ** 31, 2 ** 31 - 1)[i % 4]
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    csa2.chunk_attn(cache, q, p, s, out=out, lse=lse)
+    st, word = csa2.get_error(cache)
+    assert st == csa2.ERR_DEVICE_BOUNDS, word
+    mass = csa2.attn_mass(cache, q, p, lse, torch.zeros(2, cache.capacity, device="cuda"), s).double().cpu().numpy()
+    scale = 1 / math.sqrt(512)
+    for b, n_ctx in enumerate(lens):
+        a, z = int(start[b]), int(start[b + 1])
+        good = _without(table, page, n_ctx, bad[b])
+        seen = np.searchsorted(good, np.clip(pos[a:z].astype(np.int64) + 1, 0, n_ctx))
+        K = O.keys(table, page, codes, scales, b, n_ctx)[good]
+        ref = O.attention(q[a:z].double().cpu().numpy(), K, seen, scale)
+        tol, tol_lse = O.attention_bounds(ref, n_ctx)
+        tol = tol + torch.finfo(torch.bfloat16).eps / 2 * (np.abs(ref["out"]) + tol)
+        err = np.abs(out[a:z].double().cpu().numpy() - ref["out"])
+        assert (err <= tol).all(), f"request {b}: out off by {err.max():.3e}, {(err / np.maximum(tol, 1e-30)).max():.2f} of its bound"
+        got, none = lse[a:z].double().cpu().numpy(), ~np.isfinite(ref["lse"])
+        assert (got[none] == -np.inf).all()
+        err = np.abs(got[~none] - ref["lse"][~none])
+        assert (err <= tol_lse[~none]).all(), f"request {b}: lse off by {err.max():.3e}"
+        # a row's weights: each off by twice the scores' error and the lse's own; their sum by n 2^-24 more
+        d = 2 * ((512 + 4) * 2.0 ** -23 * ref["size"][~none] + 2.0 ** -21 + tol_lse[~none]).sum()
+        d += got[~none].size ** 2 * 2.0 ** -24 + n_ctx * 2.0 ** -24 * got[~none].size
+        assert abs(mass[b].sum() - got[~none].size) <= d
+        assert (mass[b][np.setdiff1d(np.arange(n_ctx), good)] == 0).all()

@@ -278,7 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         mx = fmaxf(mx, S.xchg[g & 1][tid ^ 64]);
         const float m_new = mx == -INFINITY ? -INFINITY : mx * c2;
         float f = 1.0f;
-        if (m_new > m_ref + kRaise || (m_ref == -INFINITY && m_new != -INFINITY)) {
+        // (the difference: above 2^27, where values are 16 apart, m_ref + kRaise can
+        // round up to the next one, and probabilities of 2^16 would leave fp16)
+        if (m_new - m_ref > kRaise) {
           f = m_ref == -INFINITY ? 0.0f : ex2(m_ref - m_new);
           m_ref = m_new;
           l *= f;

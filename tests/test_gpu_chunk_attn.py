@@ -290,3 +290,38 @@ def test_chunk_attn_leaves_bad_pages_out(csa2, lens, new, page, bad, q_scale, H)
         d += got[~none].size ** 2 * 2.0 ** -24 + n_ctx * 2.0 ** -24 * got[~none].size
         assert abs(mass[b].sum() - got[~none].size) <= d
         assert (mass[b][np.setdiff1d(np.arange(n_ctx), good)] == 0).all()
+
+
+def test_chunk_attn_maximum_rises_by_one_spacing(csa2):
+    """Scores of 2^27 to 2^28 (log2 units), where fp32 values are 16 apart, and a
+    maximum that rises by one such step from a tile to the next: the
+    probabilities stay inside fp16's range."""
+    n, H, new, key = 300, 64, 148, 256
+    cache = csa2.Cache(3, 128, [[2, 0, 1]], [n])
+    rows = torch.from_numpy(O.rows_of(np.array([[2, 0, 1]]), 128, 0, n)).cuda()
+    codes, scales = np.zeros((n, 256), np.uint8), np.full((n, 32), 0x38, np.uint8)     # scales of 1
+    scales[:, 0] = 0x58                                # 16
+    codes[:, 0] = 6                                    # channel 0: 4 x 16
+    codes[:, 8] = 2                                    # channel 16: 1
+    codes[key, 16] = 2                                 # channel 32: 1 for one key of the second tile
+    codes[:, 24] = 2                                   # channel 48: 1 (no query looks at it)
+    cache.kv_codes[rows], cache.kv_scales[rows] = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    # q . v = 2^27 (1 + j / 128) + 16, and 16 more for that key: odd and even multiples of 16.  fp32's ln 2
+    # times its log2 e rounds to 1, so the kernel's scores in log2 units are these numbers.
+    scale = float(np.float32(np.log(2.0)))
+    assert np.float32(scale) * np.float32(1.4426950408889634) == 1
+    q = torch.zeros(new, H, 512)
+    j = (torch.arange(new)[:, None] * 7 + torch.arange(H)) % 128
+    q[..., 0] = 2.0 ** 21 * (1 + j / 128)
+    q[..., 16] = q[..., 32] = 16
+    lse = torch.empty(new, H, device="cuda")
+    pos, start = torch.full((new,), n - 1, dtype=torch.int32).cuda(), torch.tensor([0, new], dtype=torch.int32).cuda()
+    out = csa2.chunk_attn(cache, q.bfloat16().cuda(), pos, start, scale=scale, lse=lse).double().cpu()
+    assert csa2.get_error(cache)[0] == csa2.OK
+    rest = (n - 1) * 2.0 ** -16                        # the other keys, next to that one
+    # P in fp16 (2^-11), the sums (n 2^-23 each), bf16's rounding
+    tol = 2.0 ** -11 + 2 * n * 2.0 ** -23 + torch.finfo(torch.bfloat16).eps / 2
+    for ch, want in ((48, 1.0), (32, 1 / (1 + rest)), (16, 1.0), (0, 64.0)):
+        assert ((out[..., ch] - want).abs() <= 1.01 * tol * want).all(), ch
+    want = scale * (2.0 ** 27 * (1 + j.double() / 128) + 32) + math.log(1 + rest)
+    assert ((lse.double().cpu() - want).abs() <= 2.0 ** -22 * want).all()

@@ -286,8 +286,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
           l *= f;
         }
         const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
-        // far from 0, s * c2 - ref has to be rounded like ref was
-        const bool careful = __any_sync(0xffffffffu, lim < key0 + 128 || !(fabsf(ref) < kFar));
+        // Far from 0, s * c2 - ref has to be rounded like ref was.  One of the two
+        // factors is 1: the row's bits are those of the plain form unless it is far
+        // itself, whatever the warp's other rows are.
+        const bool far = !(fabsf(ref) < kFar);
+        const float pre = far ? c2 : 1.0f, post = far ? 1.0f : c2;
+        const bool careful = __any_sync(0xffffffffu, lim < key0 + 128 || far);
         // the probabilities wait in registers (fp16) for the previous tile's P to be free
         uint32_t h[64];
         if (!seen) {
@@ -306,8 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
               for (int j = 0; j < 16; j += 2) {
                 const int key = key0 + c * 16 + j;
                 const float s0 = __uint_as_float(r[c & 1][j]), s1 = __uint_as_float(r[c & 1][j + 1]);
-                const float p0 = key < lim ? ex2(__fsub_rn(__fmul_rn(s0, c2), ref)) : 0.0f;
-                const float p1 = key + 1 < lim ? ex2(__fsub_rn(__fmul_rn(s1, c2), ref)) : 0.0f;
+                const float p0 = key < lim ? ex2(fmaf(__fmul_rn(s0, pre), post, -ref)) : 0.0f;
+                const float p1 = key + 1 < lim ? ex2(fmaf(__fmul_rn(s1, pre), post, -ref)) : 0.0f;
                 sum[(j >> 1) & 3] += p0 + p1;
                 h[c * 8 + (j >> 1)] = pack_half2(p0, p1);
               }

@@ -325,3 +325,29 @@ def test_chunk_attn_maximum_rises_by_one_spacing(csa2):
         assert ((out[..., ch] - want).abs() <= 1.01 * tol * want).all(), ch
     want = scale * (2.0 ** 27 * (1 + j.double() / 128) + 32) + math.log(1 + rest)
     assert ((lse.double().cpu() - want).abs() <= 2.0 ** -22 * want).all()
+
+
+@pytest.mark.parametrize("what", ["inf", "large", "masked"])
+def test_chunk_attn_rows_do_not_depend_on_each_other(csa2, what):
+    """Every fifth row is changed (an infinity, scores of 10^9, or a position that
+    sees a part only): the bits of the others stay."""
+    for seed in range(4):
+        lens, new, H = [500], [60], 16
+        args = _case(csa2, lens, new, H, 128, seed=seed, pos=[499] * 60)
+        cache, start, pos, q = args[0], args[4], args[5], args[6]
+        s, scale = torch.from_numpy(start).cuda(), 1 / math.sqrt(512)
+        lse, lse2 = torch.empty(q.shape[:2], device="cuda"), torch.empty(q.shape[:2], device="cuda")
+        out = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), s, scale=scale, lse=lse)
+        change = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+        if what == "masked":
+            change[::5] = True
+            pos[::5] = np.random.default_rng(seed).integers(0, 499, 12)
+        else:
+            change.view(-1)[::5] = True
+            if what == "inf":
+                q.view(-1, 512)[::5, 7] = float("inf")
+            else:
+                q.view(-1, 512)[::5] *= 2.0 ** 30
+        again = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), s, scale=scale, lse=lse2)
+        assert not torch.equal(out[change], again[change])
+        assert torch.equal(out[~change], again[~change]) and torch.equal(lse[~change], lse2[~change]), seed

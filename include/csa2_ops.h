@@ -111,9 +111,10 @@ CSA2_API csa2_status csa2_norm_rope_append(const csa2_cache* cache, const csa2_i
  *            aligned; its contents on entry do not matter.  Two calls in
  *            flight at once must not share it.
  * Dequantised rows are exact in fp16; scores, softmax and sums are fp32, the
- * probabilities are rounded to fp16 for the product with V.  Long contexts are
- * cut along the keys by a plan made of the lengths alone: the same lengths
- * give the same bits.
+ * probabilities are rounded to fp16 for the product with V (by 2^-11 of
+ * themselves, or by 2^-32 of the row's largest where they are below 2^-21 of it).
+ * Long contexts are cut along the keys by a plan made of the lengths alone: the
+ * same lengths give the same bits.
  * Device errors: a page id outside [0, num_pages) under a visible entry
  * (CSA2_ERR_DEVICE_BOUNDS; its entries are left out, as if the query did not
  * see them), a q_start that decreases or leaves [0, n_queries] (the request has

@@ -26,9 +26,13 @@
 // The rows are stored times 2^-8 (an E4M3 code shifted into fp16 is 2^-8 of its
 // value; the product with E2M1 stays exact in fp16, subnormals included);
 // the scores' factor and the output's carry the 2^8.
-// The running maximum is raised only when a row's new maximum is more than 2^8
-// above it (the probabilities stay below 2^8 until then, well inside fp16), so
-// that O, which lies in tensor memory, is rarely rescaled.
+// P is held in fp16 relative to a reference 2^7 below the row's maximum, and the
+// reference is raised only when a row's new maximum is more than 2^15 above it:
+// P stays below 2^15, inside fp16, and O, which lies in tensor memory, is rarely
+// rescaled.  The 2^7 are for the other end: weights down to 2^-32 of the largest
+// count in P as they do in the fp32 sum.  With a reference at the maximum itself
+// they were lost from 2^-25 on: of 262,143 equal entries 17.4 nats below one other,
+// all (0.7 % of the weight).  The room costs one subtraction a tile.
 //
 // 1,024 tokens x 64 heads over 32,768 entries: 3.85 ms, 0.67 of the tensor cores'
 // measured rate; one token of 8 requests x 64 heads over 65,536: 160 us with the
@@ -62,7 +66,7 @@ struct RangeRecord {
 // Workspace: the records, then two partial results per pair (the tile that
 // the range starts inside, the tile that it ends inside): 512 sums of each of
 // 128 rows, four channels of all rows together (the writers' lanes are rows),
-// then the rows' maxima (log2) and their sums.
+// then the rows' references (log2) and their sums.
 struct ChunkWorkspace {
   RangeRecord* rec;
   float* part;
@@ -79,7 +83,7 @@ __host__ __device__ inline float* partial_of(const ChunkWorkspace& w, int pair, 
   return w.part + (2 * static_cast<size_t>(pair) + which) * kPartialFloats;
 }
 __host__ __device__ inline int partial_at(int row, int ch) { return ((ch >> 2) * kPairRows + row) * 4 + (ch & 3); }
-constexpr int kPartialMax = kPairRows * kKvDim, kPartialSum = kPartialMax + kPairRows;
+constexpr int kPartialRef = kPairRows * kKvDim, kPartialSum = kPartialRef + kPairRows;
 
 constexpr int kGSoftWarps = 4, kGDeqWarps = 8;
 constexpr int kGThreads = (kGSoftWarps + kGDeqWarps + 1) * 32;   // 416
@@ -93,7 +97,8 @@ constexpr uint32_t kOCol = 0, kSCol = 256;   // O: 2 x 128 columns; S: 2 buffers
 constexpr uint32_t kIdescS = idesc_f16_f32(128, 256, false, false);
 constexpr uint32_t kIdescO = idesc_f16_f32(128, 256, false, true);
 constexpr int kBarSoft = 1;
-constexpr float kRaise = 8.0f;               // log2 units a maximum may rise before O is rescaled
+constexpr float kBelow = 7.0f;               // log2 units from a row's maximum down to a new reference
+constexpr float kRaise = kBelow + 8.0f;      // ... that a maximum may lie above the reference
 constexpr int kStageRow = kKvDim * 2 + 16;     // bytes between staged output rows
 constexpr float kFar = 1048576.0f;           // 2^20: fp32 values are less than 1/8 apart below it
 
@@ -281,8 +286,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         // (the difference: above 2^27, where values are 16 apart, m_ref + kRaise can
         // round up to the next one, and probabilities of 2^16 would leave fp16)
         if (m_new - m_ref > kRaise) {
-          f = m_ref == -INFINITY ? 0.0f : ex2(m_ref - m_new);
-          m_ref = m_new;
+          f = m_ref == -INFINITY ? 0.0f : ex2(m_ref - (m_new - kBelow));
+          m_ref = m_new - kBelow;
           l *= f;
         }
         const float ref = m_ref == -INFINITY ? 0.0f : m_ref;
@@ -409,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       }
       if (khalf == 0 && pr < rows) {
         if (!whole) {
-          part[kPartialMax + pr] = m_ref;
+          part[kPartialRef + pr] = m_ref;
           part[kPartialSum + pr] = l;
         } else if (lse != nullptr) {
           lse[orow] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
@@ -712,13 +717,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   const int k = threadIdx.x;
   const int parts = 1 + __syncthreads_count(k >= c && k < r.pairs && wsp.rec[min(k, r.pairs - 1)].lo < r.tile_hi);
   auto part_of = [&](int i) { return partial_of(wsp, c - 1 + i, i == 0 ? 1 : 0); };
-  // the rows' maxima and sums: the warps share the parts, so that all of a row's
+  // the rows' references and sums: the warps share the parts, so that all of a row's
   // loads are in flight together
   float m = -INFINITY;
 #pragma unroll 4
   for (int i = warp; i < parts; i += kJoinWarps) {
     const float* part = part_of(i);
-    factor[i][lane] = part[kPartialMax + row];       // (rows that are not there: never used)
+    factor[i][lane] = part[kPartialRef + row];       // (rows that are not there: never used)
     total[i][lane] = part[kPartialSum + row];
     m = fmaxf(m, factor[i][lane]);
   }

@@ -351,3 +351,44 @@ def test_chunk_attn_rows_do_not_depend_on_each_other(csa2, what):
         again = csa2.chunk_attn(cache, q, torch.from_numpy(pos).cuda(), s, scale=scale, lse=lse2)
         assert not torch.equal(out[change], again[change])
         assert torch.equal(out[~change], again[~change]) and torch.equal(lse[~change], lse2[~change]), seed
+
+
+@pytest.mark.parametrize("new", [2, 148])
+def test_chunk_attn_long_tail_of_small_weights(csa2, new):
+    """One entry 8 to 24 nats above 262,143 equal ones: the tail's weights count
+    in the product with V as they do in the sum, in tiles that one range holds
+    whole (148 tokens x 64 heads are a tile for each of 74 ranges) and in cut ones.
+
+    Bounds: a score is one exact product, its factor and the reference are off by
+    at most 2^-23 of 40 log2 units together, exp2 by 2^-22: 1e-5 for a weight, as
+    much for the sum.  P is rounded to fp16 by 2^-11 of itself, or, below
+    fp16's normal range, by 2^-25 where the row's largest P is at least 2^7:
+    2^-32 of the largest weight for each of the n entries.  O takes 16 keys at a
+    time, each sum off by at most 2^-22 of it; the fp32 row sum n / 256 roundings.
+    """
+    n, H, page = 1 << 18, 64, 4096
+    cache = csa2.Cache(n // page, page, np.random.default_rng(3).permutation(n // page).astype(np.int32)[None], [n])
+    first = int(cache.page_table[0, 0]) * page
+    cache.kv_scales.fill_(0x38)                        # scales of 1
+    cache.kv_codes[:, 8] = 2                           # channel 16: 1 for every entry
+    cache.kv_codes[:, 16] = 2                          # channel 32: 1 for all but the first
+    cache.kv_codes[first, 16] = 0
+    cache.kv_codes[first, 0] = 2                       # channel 0: 1 for the first
+    q = torch.zeros(new, H, 512)
+    q[..., 0] = torch.linspace(8, 24, new * H).view(new, H)
+    q = q.bfloat16()
+    gap = q[..., 0].double()
+    lse = torch.empty(new, H, device="cuda")
+    pos, start = torch.full((new,), n - 1, dtype=torch.int32).cuda(), torch.tensor([0, new], dtype=torch.int32).cuda()
+    out = csa2.chunk_attn(cache, q.cuda(), pos, start, scale=1.0, lse=lse).double().cpu()
+    assert csa2.get_error(cache)[0] == csa2.OK
+    tail = (n - 1) * torch.exp(-gap)
+    top = 1 / (1 + tail)                               # the first entry's weight
+    rel = 2e-5 + 2.0 ** -11 + n / 16 * 2.0 ** -22 + n / 256 * 2.0 ** -24
+    for ch, want, low in ((0, top, 0.0), (32, tail * top, 1.0), (16, torch.ones_like(top), 1.0)):
+        tol = rel * want + low * n * 2.0 ** -32 * top
+        tol = tol + torch.finfo(torch.bfloat16).eps / 2 * (want + tol)
+        err = (out[..., ch] - want).abs()
+        assert (err <= tol).all(), f"channel {ch}: {float((err / tol).max()):.2f} of its bound, worst at {float(gap.flatten()[(err / tol).argmax()])} nats"
+    want = gap + torch.log1p(tail)
+    assert ((lse.double().cpu() - want).abs() <= 2e-5 + n / 256 * 2.0 ** -24 + 2.0 ** -23 * want).all()

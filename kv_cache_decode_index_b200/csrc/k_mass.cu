@@ -54,11 +54,16 @@ constexpr int kMaxPairs = 128;
 constexpr int kBarEpi = 1, kBarDeq = 2;
 
 // Queries are scaled by 2^6 in fp16 while every magnitude of a row tile is below
-// 2^9 and every log-sum-exp fits; other tiles ("wide") scale each row by itself
-// and take factors and log-sum-exp per column.
+// 2^9, every log-sum-exp fits and the unit of an accumulator is between 0.01 and 8
+// log2 units (scales of 0.002 to 1.4); other tiles ("wide") scale each row by
+// itself and take factors and log-sum-exp per column.  Why 8: below fp16's normal
+// range a query channel is off by up to 2^-31, which a larger scale, made for
+// small queries, would carry into the scores.  Up to it the error of a score is
+// below 512 x 2^-31 x 1.4 of the entry's largest channel (1.4 x 2^-22 of it).
 constexpr int kMExponent = 8;
 constexpr float kMUndo = kRowScale / 64.0f;       // of 2^6 and of the entries' 2^-8
 constexpr float kMLargest = 60000.0f;
+constexpr float kMUnitLow = 0.01f, kMUnitHigh = 8.0f;
 
 // kMRows: query rows of a tile (both CTAs); kMRing: pairs of slots of entries.
 template <int kMRows, int kMRing, int kMStages>
@@ -322,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
           const int turn = loads & 1;
           if (tid == 0) S.wide[turn ^ 1] = 0.0f;        // (the other CTA writes it after it has heard of this turn)
           // this CTA's half of the rows; the column tables hold both halves
-          bool large = !(c2 > 0.01f);
+          bool large = !(c2 > kMUnitLow && c2 < kMUnitHigh);
           const int mine = in_tile - static_cast<int>(rank) * half;
           load_query_rows<kMRows / 2, kMEpiWarps, kMExponent>(q, row0 + static_cast<int>(rank) * half, mine, half, sign, S.q[0],
                                                        warp, lane, [&](int, uint32_t top) {
@@ -340,7 +345,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
             S.col_lim[c] = lim;
             S.col_lse2[c] = l * kLog2e;
             // -lse in the accumulator's unit: three fp16 parts hold an fp32 value
-            // whole (columns without a row: far below everything)
+            // whole, or to 2^-25 below 1/2 (columns without a row: far below
+            // everything)
             float v = c < in_tile ? (lim > 0 ? -l * (kLog2e / c2) : 0.0f) : -kMLargest;
             if (!(fabsf(v) <= kMLargest)) large = true, v = 0.0f;
             const int r = c - static_cast<int>(rank) * half;

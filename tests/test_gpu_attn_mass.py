@@ -269,3 +269,32 @@ def test_attn_mass_wait_limit_single_tokens(csa2):  # noqa: F811
     st, word = csa2.get_error(cache)
     assert st == csa2.OK, word
     _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
+def test_attn_mass_small_queries_large_scale(csa2):  # noqa: F811
+    """Queries times 2^-30 with a scale times 2^30: the weights are those of the
+    queries and the scale as they were."""
+    lens, new, H = [300, 200], [40, 7], 16
+    case = _case(csa2, lens, new, H, 128, seed=8)
+    cache, _, _, _, start, pos, q = case
+    q.mul_(2.0 ** -30)
+    scale = 2.0 ** 30 / math.sqrt(512)
+    lse, want, tol = _reference(case, lens, 1, scale)
+    mass = torch.zeros(2, cache.capacity, device="cuda")
+    csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(start).cuda(), scale=scale)
+    assert csa2.get_error(cache)[0] == csa2.OK
+    _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
+@pytest.mark.parametrize("factor", [2.0 ** 4, 2.0 ** 5, 2.0 ** 8, 2.0 ** 20])
+def test_attn_mass_scales_on_both_sides_of_the_forms(csa2, factor):  # noqa: F811
+    """The same product of queries and scale, split differently."""
+    lens, new, H = [300, 200], [40, 7], 16
+    case = _case(csa2, lens, new, H, 128, seed=8)
+    cache, _, _, _, start, pos, q = case
+    q.div_(factor)
+    scale = factor / math.sqrt(512)
+    lse, want, tol = _reference(case, lens, 1, scale)
+    mass = torch.zeros(2, cache.capacity, device="cuda")
+    csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(start).cuda(), scale=scale)
+    _check(mass, torch.zeros_like(mass), want, tol, lens)

@@ -88,7 +88,7 @@ struct __align__(1024) MassSmem {
   uint64_t acc_full[kMAcc];
   uint64_t acc_empty[kMAcc];                      // leader
   uint64_t q_full;                                // leader
-  uint64_t scale_full;                            // what the other CTA says of its rows has arrived
+  uint64_t scale_full[2];                         // what the other CTA says of its rows has arrived (by turns)
   uint64_t drain;
   uint64_t stage_full[kMStages + 1];
   int stage_row[kMStages + 1];                    // a stage's cache row, -1: not there, -2: no tile
@@ -159,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       mbar_init(&S.acc_empty[i], 2 * kMEpiWarps);
     }
     mbar_init(&S.q_full, 2 * kMEpiWarps);
-    mbar_init(&S.scale_full, kMEpiWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&S.scale_full[i], kMEpiWarps);
     mbar_init(&S.drain, 1);
     S.wide[0] = S.wide[1] = 0.0f;
     fence_barrier_init();
@@ -297,11 +297,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMThreads, 1)
       }
     };
     // Tells the other CTA (its warps wait for all of this CTA's) and hears from
-    // it; whether one warp's wait ran out is voted on, so that all four leave.
+    // it; whether one warp's wait ran out is voted on, so that all four leave.  Two
+    // barriers by turns: the other CTA can be at the next exchange before a warp
+    // here has looked at this one, and with one barrier that warp would wait for a
+    // parity that has gone by.  It cannot be two ahead, since that takes this
+    // CTA's arrivals for the next one, which follow the vote.
     auto exchange = [&]() {
+      uint64_t* heard = &S.scale_full[told & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(&S.scale_full), rank ^ 1u));
-      ok = mbar_wait_cluster_all(&S.scale_full, told & 1, wait_ns);
+      if (lane == 0) mbar_arrive_release_cluster(map_rank(smem_u32(heard), rank ^ 1u));
+      ok = mbar_wait_cluster_all(heard, (told >> 1) & 1, wait_ns);
       ok = !named_bar_or(kBarEpi, kMEpiWarps * 32, !ok);
       ++told;
     };

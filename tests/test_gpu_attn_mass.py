@@ -298,3 +298,20 @@ def test_attn_mass_scales_on_both_sides_of_the_forms(csa2, factor):  # noqa: F81
     mass = torch.zeros(2, cache.capacity, device="cuda")
     csa2.attn_mass(cache, q, torch.from_numpy(pos).cuda(), lse, mass, torch.from_numpy(start).cuda(), scale=scale)
     _check(mass, torch.zeros_like(mass), want, tol, lens)
+
+
+def test_attn_mass_many_wide_tiles(csa2):  # noqa: F811
+    """Row tiles that all take the wide form, whose CTAs tell each other twice a
+    tile, in many launches: no wait runs out, and the bits are the same."""
+    lens, new, H = [260, 130], [200, 120], 16
+    case = _case(csa2, lens, new, H, 128, seed=11)
+    cache, _, _, _, start, pos, q = case
+    scale = 1e-4                                  # below the common scale's range
+    lse, want, tol = _reference(case, lens, 1, scale)
+    p, s = torch.from_numpy(pos).cuda(), torch.from_numpy(start).cuda()
+    first = csa2.attn_mass(cache, q, p, lse, torch.zeros(2, cache.capacity, device="cuda"), s, scale=scale)
+    _check(first, torch.zeros_like(first), want, tol, lens)
+    for _ in range(200):
+        again = csa2.attn_mass(cache, q, p, lse, torch.zeros_like(first), s, scale=scale)
+        assert torch.equal(first, again)
+    assert csa2.get_error(cache)[0] == csa2.OK

@@ -159,3 +159,39 @@ def test_capacities_above_2_30_are_refused(lib):  # noqa: F811
     c, _ = _cache(lib, page_size=2 ** 20, num_pages=4, max_pages_per_req=1024)
     assert evict(c, 2 ** 30 + 1) == lib.ERR_SHAPE
     assert b"2^30" in lib._lib.csa2_last_error_message()
+
+
+def test_mass_exchange_is_not_overrun():
+    """Every order of steps of attn_mass's exchange() between two CTAs (two warps
+    each, four exchanges one after the other), with as many barriers by turns as
+    the kernel declares: no barrier completes a second phase while a warp still
+    waits for the one before, whose parity it would then miss."""
+    text = open(os.path.join(ROOT, "kv_cache_decode_index_b200", "csrc", "k_mass.cu")).read()
+    found = re.search(r"uint64_t scale_full(?:\[(\d+)\])?;", text)
+    turns, warps, rounds = int(found.group(1) or 1), 2, 4
+    # a warp's place: 2 k before its arrival for exchange k, 2 k + 1 before its look at it; the vote
+    # lets a warp go on once its CTA's warps have all looked
+    start = ((0,) * warps,) * 2
+    todo, known = [start], {start}
+    while todo:
+        state = todo.pop()
+        for c in range(2):
+            for w in range(warps):
+                k, looks = divmod(state[c][w], 2)
+                if k == rounds:
+                    continue
+                if looks:
+                    mine = [j for j in range(rounds) if j % turns == k % turns]          # this barrier's exchanges
+                    arrived = sum(p > 2 * j for p in state[1 - c] for j in mine)
+                    done, phase = arrived // warps, k // turns
+                    assert done <= phase + 1, f"exchange {k}: {done} phases are over, {phase} is awaited"
+                    if done == phase:
+                        continue                      # it waits
+                elif any(p < 2 * k for p in state[c]):
+                    continue                          # the vote: another warp has not looked yet
+                place = tuple(p + (i == w) for i, p in enumerate(state[c]))
+                after = (place, state[1]) if c == 0 else (state[0], place)
+                if after not in known:
+                    known.add(after)
+                    todo.append(after)
+    assert ((2 * rounds,) * warps,) * 2 in known

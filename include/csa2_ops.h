@@ -169,8 +169,9 @@ CSA2_API csa2_status csa2_attn_mass(const csa2_cache* cache, int32_t n_queries, 
  *              mass (requests that are moved, their first `budget` values)
  *   ik4        the FP4 indexer keys to move with the rows, or NULL
  *   workspace  at least csa2_evict_workspace_bytes bytes, 16-byte aligned
- * kept, new_len and mass_out overlap no input.  ctx_len and the page table are
- * not modified: the caller continues with dst_pages and new_len for the
+ * kept, new_len, mass_out and the workspace overlap neither mass, dst_pages, the
+ * page table or ctx_len nor one another (refused).  ctx_len and the page table
+ * are not modified: the caller continues with dst_pages and new_len for the
  * requests that were moved and frees their old pages.
  * Device errors: CSA2_ERR_DEVICE_BOUNDS for a bad page (the row is not moved)
  * or ctx_len (the request counts as empty).

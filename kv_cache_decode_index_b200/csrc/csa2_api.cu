@@ -193,8 +193,14 @@ csa2_status check_dense(const csa2_cache* c, int n_queries, const int32_t* q_sta
 // Whether [a, a + a_bytes) and [b, b + b_bytes) meet.
 bool overlap(const void* a, unsigned long long a_bytes, const void* b, unsigned long long b_bytes) {
   const unsigned long long x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + b_bytes && y < x + a_bytes;
+  return a_bytes > 0 && b_bytes > 0 && x < y + b_bytes && y < x + a_bytes;
 }
+// An argument's bytes.
+struct Range {
+  const char* name;
+  const void* at;
+  unsigned long long bytes;
+};
 
 csa2_status check_workspace(const void* ws, size_t bytes, size_t need, const char* fn) {
   if (ws == nullptr || !aligned(ws, 16)) return fail(CSA2_ERR_ARG, "workspace must be set and 16-byte aligned");
@@ -719,11 +725,25 @@ csa2_status csa2_evict(const csa2_cache* cache, const csa2_ik4* ik4, const float
     return fail(CSA2_ERR_SHAPE, "batch * budget must stay below 2^31");
   if (mass == nullptr || dst_pages == nullptr || kept == nullptr || new_len == nullptr)
     return fail(CSA2_ERR_ARG, "mass, dst_pages, kept and new_len must be set");
-  if (mass_out == mass) return fail(CSA2_ERR_ARG, "mass_out must not be mass");
-  if (new_len == cache->ctx_len) return fail(CSA2_ERR_ARG, "new_len must not be the cache's ctx_len");
   if (dst_pages == cache->page_table) return fail(CSA2_ERR_ARG, "dst_pages must not be the cache's page table");
   CSA2_TRY(check_workspace(workspace, workspace_bytes, csa2_evict_workspace_bytes(cache->num_pages),
                            "csa2_evict_workspace_bytes"));
+  // what is written meets nothing that is read, nor one another
+  const unsigned long long B = cache->batch, capacity = capacity_of(cache);
+  const Range written[] = {{"kept", kept, 4 * B * budget},
+                           {"new_len", new_len, 4 * B},
+                           {"mass_out", mass_out, mass_out ? 4 * B * dst_width * cache->page_size : 0},
+                           {"workspace", workspace, csa2_evict_workspace_bytes(cache->num_pages)}};
+  const Range read[] = {{"mass", mass, 4 * B * capacity},
+                        {"dst_pages", dst_pages, 4 * B * dst_width},
+                        {"page_table", cache->page_table, 4 * B * cache->max_pages_per_req},
+                        {"ctx_len", cache->ctx_len, 4 * B}};
+  for (const Range& w : written) {
+    for (const Range& r : read)
+      if (overlap(w.at, w.bytes, r.at, r.bytes)) return fail(CSA2_ERR_ARG, "%s overlaps %s", w.name, r.name);
+    for (const Range& o : written)
+      if (&o != &w && overlap(w.at, w.bytes, o.at, o.bytes)) return fail(CSA2_ERR_ARG, "%s overlaps %s", w.name, o.name);
+  }
   DeviceInfo d;
   CSA2_TRY(device_info(&d));
   const cudaError_t e = csa2::launch_evict(*cache, ik4, mass, budget, sink, recent, dst_pages, dst_width, kept, new_len,

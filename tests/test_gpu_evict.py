@@ -232,3 +232,25 @@ def test_evict_many_requests(csa2):
                                recent=99, mass_out=mass_out)
     assert csa2.get_error(cache)[0] == csa2.OK
     _check(csa2, cache, table, dst, k4, mass, before, kept, new_len, mass_out, lens, budget, 3, 99)
+
+
+def test_evict_neighbouring_buffers(csa2):
+    """Inputs and outputs that touch in one buffer, without a gap."""
+    budget, page = 100, 128
+    cache, table, dst, _, rng = _setup(csa2, [300, 500], budget, page, 3)
+    cap, width = cache.capacity, dst.shape[1]
+    mass = rng.random((2, cap)).astype(np.float32)
+    before = _rows(csa2, cache, None)
+    sizes = [2 * cap, 2 * width * page, 2 * budget, 2, 2 * width, 2]
+    buf = torch.zeros(sum(sizes), dtype=torch.int32, device="cuda")
+    m, mass_out, kept, new_len, pages, ctx = torch.split(buf, sizes)
+    m, mass_out, kept = m.view(torch.float32).view(2, cap), mass_out.view(torch.float32).view(2, -1), kept.view(2, budget)
+    pages = pages.view(2, width)
+    m.copy_(torch.from_numpy(mass))
+    mass_out.fill_(7.0)
+    pages.copy_(torch.from_numpy(dst))
+    ctx.copy_(cache.ctx_len)
+    cache.ctx_len = ctx
+    csa2.evict(cache, m, budget, pages, sink=3, recent=20, kept=kept, new_len=new_len, mass_out=mass_out)
+    assert csa2.get_error(cache)[0] == csa2.OK
+    _check(csa2, cache, table, dst, None, mass, before, kept, new_len, mass_out, [300, 500], budget, 3, 20)

@@ -195,3 +195,30 @@ def test_mass_exchange_is_not_overrun():
                     known.add(after)
                     todo.append(after)
     assert ((2 * rounds,) * warps,) * 2 in known
+
+
+def test_evict_refuses_overlaps(lib):  # noqa: F811
+    """Outputs and workspace that share bytes with an input or with one another:
+    equal, shifted, or by one element.  (Every call is one that is refused.)"""
+    _, p = _cache(lib)
+    # mass 2 x 256 floats, dst_pages 2 x 1, page_table 2 x 2, ctx_len 2, kept 2 x 100, new_len 2, mass_out 2 x 128 floats
+    at = {"mass": p, "dst_pages": p + 4096, "page_table": p + 4112, "ctx_len": p + 4144, "kept": p + 8192,
+          "new_len": p + 9216, "mass_out": p + 12288, "workspace": p + 16384}
+    size = {"mass": 2048, "dst_pages": 8, "page_table": 16, "ctx_len": 8, "kept": 800, "new_len": 8, "mass_out": 1024,
+            "workspace": 16}
+    outs, ins = ("kept", "new_len", "mass_out", "workspace"), ("mass", "dst_pages", "page_table", "ctx_len")
+    V = ctypes.c_void_p
+
+    def call(places):
+        c, _ = _cache(lib, page_table=places["page_table"], ctx_len=places["ctx_len"])
+        return lib._lib.csa2_evict(ctypes.byref(c), None, V(places["mass"]), 100, 1, 9, V(places["dst_pages"]), 1,
+                                   V(places["kept"]), V(places["new_len"]), V(places["mass_out"]), V(places["workspace"]),
+                                   16, None)
+    for w in outs:
+        for o in ins + outs:
+            if o == w:
+                continue
+            unit = 16 if w == "workspace" else 4
+            for where in (at[o], at[o] + (size[o] - 1) // unit * unit, at[o] - (size[w] - 1) // unit * unit):
+                assert call({**at, w: where}) == lib.ERR_ARG, (w, o)
+                assert b"overlaps" in lib._lib.csa2_last_error_message(), (w, o)

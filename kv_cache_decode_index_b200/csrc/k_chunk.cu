@@ -52,7 +52,7 @@ namespace csa2 {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxPairs = 148;               // ranges of one launch
+constexpr int kMaxPairs = 74;                // ranges of one launch: pairs of CTAs on 148 SMs
 constexpr int kPairRows = 128;               // query rows of a tile
 
 // What a pair says of its range, for the launch that joins cut tiles.
@@ -77,6 +77,7 @@ __host__ __device__ inline ChunkWorkspace split_chunk_ws(void* ws) {
   w.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kMaxPairs * sizeof(RangeRecord));
   return w;
 }
+static_assert(kMaxPairs * sizeof(RangeRecord) % 16 == 0, "partial results are read 16 bytes at a time");
 constexpr size_t kPartialFloats = static_cast<size_t>(kPairRows) * (kKvDim + 2);
 // Partial result `which` (0: tile started inside, 1: tile ended inside) of a pair.
 __host__ __device__ inline float* partial_of(const ChunkWorkspace& w, int pair, int which) {

@@ -50,7 +50,7 @@ constexpr int kMPart = 32;                        // tiles of entries whose sums
 constexpr int kMSlot = 128 * 128;                 // 128 rows x 64 channels
 constexpr int kMStage = 128 * (kKvCodeBytes + kKvScaleBytes);   // 128 packed entries
 constexpr int kMAcc = 2;
-constexpr int kMaxPairs = 128;
+constexpr int kMaxPairs = 74;                     // ranges of one launch: pairs of CTAs on 148 SMs
 constexpr int kBarEpi = 1, kBarDeq = 2;
 
 // Queries are scaled by 2^6 in fp16 while every magnitude of a row tile is below

@@ -222,3 +222,11 @@ def test_evict_refuses_overlaps(lib):  # noqa: F811
             for where in (at[o], at[o] + (size[o] - 1) // unit * unit, at[o] - (size[w] - 1) // unit * unit):
                 assert call({**at, w: where}) == lib.ERR_ARG, (w, o)
                 assert b"overlaps" in lib._lib.csa2_last_error_message(), (w, o)
+
+
+def test_dense_workspaces_hold_what_a_launch_can_touch(lib):  # noqa: F811
+    """Two partial results for each of 74 pairs of CTAs, and a record of at most 64
+    bytes: 128 rows x (512 sums, reference, sum), or 8,192 weights."""
+    for batch, n, H in ((1, 1, 16), (8, 8, 64), (1024, 2 ** 20, 64)):
+        assert lib._lib.csa2_chunk_attn_workspace_bytes(batch, n, H) <= 74 * (2 * 128 * 514 * 4 + 64)
+        assert lib._lib.csa2_attn_mass_workspace_bytes(batch, n, H) <= 74 * (2 * 8192 * 4 + 64)

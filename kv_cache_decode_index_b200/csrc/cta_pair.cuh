@@ -153,17 +153,6 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
       "h"(static_cast<uint16_t>(3))
       : "memory");
 }
-// 2-D tiled load into this CTA's shared memory whose bytes are counted on a
-// barrier of either CTA of the pair (address from map_rank).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "l"(policy)
-      : "memory");
-}
-
 // Instruction descriptor of kind::f16: A = B = fp16 (bf16 when `bf16`), fp32
 // D, shape M x N; A K-major, B K-major or (b_mn) MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool bf16, bool b_mn) {

@@ -34,10 +34,11 @@
 // they were lost from 2^-25 on: of 262,143 equal entries 17.4 nats below one other,
 // all (0.7 % of the weight).  The room costs one subtraction a tile.
 //
-// 1,024 tokens x 64 heads over 32,768 entries: 3.85 ms, 0.67 of the tensor cores'
-// measured rate; one token of 8 requests x 64 heads over 65,536: 160 us with the
-// join.  A step of 256 keys takes 6,800 to 7,500 cycles against 4,096 of
-// products; what bounds it is the shared-memory pipe (72 % of its wavefronts are
+// 1,024 tokens x 64 heads over 32,768 entries: 3.92 ms for a call by itself, 0.66 of
+// the tensor cores' measured rate, and 4.31 ms in calls back to back (0.60), where
+// the power limit lowers the clock; one token of 8 requests x 64 heads over 65,536:
+// 163 us with the join.  A step of 256 keys takes 6,800 to 7,500 cycles against
+// 4,096 of products; what bounds it is the shared-memory pipe (72 % of its wavefronts are
 // taken: two dequantised operands, the probabilities, the score tiles).
 // Taking the maximum and the probabilities in one pass over the score tile, with
 // a repeat when a maximum rises, was slower (4.11 ms).
@@ -231,6 +232,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
       const int seen_keys = real ? seen_by(a.q_pos[T.q0 + own / a.heads], a.ratio, T.ctx) : T.keys;
       // A tile's keys of this thread lie on one page; its id is looked up a tile
       // ahead.  Keys under a bad one take no part (the dequantisation records it).
+      // The look-up costs a long chunk 0.9 %; one scan of the segment's pages with
+      // look-ups only where it finds a bad one cost 1.1 %, and up to 7 % in calls of
+      // its own or with its result in shared memory.
       auto page_of = [&](int t) {
         const int key = (first + t) * kGKeys + khalf * 128;
         return key < T.keys ? cache.page_table[static_cast<long long>(T.b) * cache.max_pages_per_req + key / cache.page_size]

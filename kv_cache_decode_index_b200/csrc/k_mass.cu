@@ -30,10 +30,12 @@
 // part's sums in shared memory over all row tiles.  Parts that ranges cut are
 // joined in a fixed order by a second launch.
 //
-// 512 tokens x 64 heads of two requests over 16,384 entries: 0.95 ms, 0.69 of the
-// tensor cores' measured rate; 8 single tokens x 64 heads over 65,536: 91 us.
-// What bounds it is the dequantisation (5,000 to 7,000 cycles for a tile's 128
-// entries a CTA, against 4,096 of products with 256 rows).
+// 512 tokens x 64 heads of two requests over 16,381 entries (two tokens an entry):
+// 0.95 ms for a call by itself, 0.69 of the tensor cores' measured rate, and 1.02 to
+// 1.03 ms in calls back to back (0.64), where the power limit lowers the clock; 8
+// single tokens x 64 heads over 65,536: 92 us.  What bounds it is the
+// dequantisation of a tile's 128 entries a CTA: 5,000 to 7,000 cycles against 4,096
+// of products in tiles of 256 rows, 4,700 against 1,500 in tiles of 64.
 #include <cuda_bf16.h>
 
 #include "launch.h"
@@ -745,7 +747,10 @@ cudaError_t launch_attn_mass(const csa2_cache& cache, int n_queries, const int32
   // and the room in shared memory for stages of packed entries and a third pair
   // of slots.  One token of 8 requests x 64 heads over 65,536 entries: 91 us, with
   // tiles of 256 rows 104; with 128 rows a request the narrow tiles read the
-  // entries twice: 166 us against 121 (8 x 2 tokens x 64 heads over 65,536).
+  // entries twice: 166 us against 121 (8 x 2 tokens x 64 heads over 65,536).  The
+  // host knows the average alone.  64 requests of 16,384 entries, 64 tokens x 64
+  // heads, narrow / 256 rows: one token each 185 / 208, 30 single tokens and a chunk
+  // of 34 in one request 185 / 179, all 64 in one request 173 / 105.
   const bool narrow = static_cast<long long>(n_queries) * H <= 64LL * cache.batch;
   const __nv_bfloat16* q16 = reinterpret_cast<const __nv_bfloat16*>(q);
   cudaError_t e = narrow ? launch_mass<64, 3, 2>(a, q16, scale, lse, mass, ws, pairs, wait_ns, stream)

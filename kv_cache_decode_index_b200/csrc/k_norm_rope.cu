@@ -498,7 +498,10 @@ cudaError_t launch_norm_rope(int n_rows, int heads, int dim, const void* x, csa2
   // Rows a warp holds at once: two where there are rows enough to fill the GPU
   // with such blocks, else one.  Measured with 32 heads x 128 channels, bf16 to
   // fp32, two rows / one: 8 tokens 2.8 / 2.4 us, 256 tokens 3.4 / 3.4, 512 tokens
-  // 4.4 / 5.1, 8,192 tokens 42 / 51.
+  // 4.4 / 5.1, 8,192 tokens 42 / 51.  Rows of 512 channels go one at a time: two take
+  // more than the 64 registers that four blocks an SM leave.  64 heads, bf16 to bf16,
+  // two rows (with those spills) / one: 8 tokens 9.2 / 7.2 us, 512 tokens 23.6 / 23.5,
+  // 2,048 tokens 67 / 69, 8,191 tokens 241 / 255 (memory alone: 164).
   const bool many = static_cast<long long>(n_rows) * heads * dim >= (1LL << 21);
   if (dim == 128)
     return many ? launch_nr_types<128, 2>(n_rows, heads, x, x_type, x_stride, weight, eps, rope, pos, out, out_type, stream)

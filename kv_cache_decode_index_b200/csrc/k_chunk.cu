@@ -38,8 +38,9 @@
 // the tensor cores' measured rate, and 4.31 ms in calls back to back (0.60), where
 // the power limit lowers the clock; one token of 8 requests x 64 heads over 65,536:
 // 163 us with the join.  A step of 256 keys takes 6,800 to 7,500 cycles against
-// 4,096 of products; what bounds it is the shared-memory pipe (72 % of its wavefronts are
-// taken: two dequantised operands, the probabilities, the score tiles).
+// 4,096 of products; what bounds it is the shared-memory pipe (70 % of its
+// wavefronts are taken: two dequantised operands, the probabilities, the score
+// tiles).
 // Taking the maximum and the probabilities in one pass over the score tile, with
 // a repeat when a maximum rises, was slower (4.11 ms).
 #include <cuda_bf16.h>
